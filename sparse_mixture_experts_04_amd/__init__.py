@@ -14,5 +14,7 @@ from ._lib import (MOE_BF16, MOE_ERR_HIP, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORT
                    moe_expert_up,
                    moe_expert_up_gather, moe_expert_up_gather_supported, moe_forward, moe_route, moe_route_stats,
                    moe_workspace_size, moe_route_ranked, moe_dispatch_reroute, moe_forward_reroute, moe_forward_noalloc, NOALLOC_MAX_WORKSPACE_BYTES,
+                   MOE_MXFP4, MOE_MXFP8, MOE_OP_EXPERT_FFN_MX, MOE_OP_FORWARD_MX, moe_mx_quantize, moe_mx_dequantize,
+                   moe_add_rmsnorm, moe_expert_up_mx, moe_expert_down_mx, moe_expert_ffn_mx, moe_forward_mx,
                    status_string, version)
-from .layer import ForwardBuffers, MoELayer  # noqa: F401
+from .layer import ForwardBuffers, MoELayer, MxMoELayer, mx_quantize, mx_dequantize  # noqa: F401

@@ -32,6 +32,11 @@ MOE_OP_ROUTE = 3
 MOE_OP_ROUTE_STATS = 4
 MOE_OP_DISPATCH_REROUTE = 5
 MOE_OP_FORWARD_REROUTE = 6
+MOE_OP_EXPERT_FFN_MX = 7
+MOE_OP_FORWARD_MX = 8
+
+MOE_MXFP4 = 0  # e2m1 codes, two to a byte
+MOE_MXFP8 = 1  # e4m3 codes
 
 NOALLOC_MAX_WORKSPACE_BYTES = 64 << 20  # MOE_NOALLOC_MAX_WORKSPACE_BYTES of include/moe.h
 
@@ -40,7 +45,8 @@ EXPORTED = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_capac
             "moe_route_stats", "moe_dispatch",
             "moe_expert_up", "moe_expert_up_gather", "moe_expert_up_gather_supported", "moe_expert_down",
             "moe_expert_ffn", "moe_combine", "moe_forward", "moe_route_ranked", "moe_dispatch_reroute",
-            "moe_forward_reroute", "moe_forward_noalloc")
+            "moe_forward_reroute", "moe_forward_noalloc", "moe_mx_quantize", "moe_mx_dequantize", "moe_add_rmsnorm",
+            "moe_expert_up_mx", "moe_expert_down_mx", "moe_expert_ffn_mx", "moe_forward_mx")
 
 
 class MoeConfig(ctypes.Structure):
@@ -88,6 +94,16 @@ def _load():
         "moe_forward_reroute": (ctypes.c_int, [CFG, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t,
                                                P]),
         "moe_forward_noalloc": (ctypes.c_int, [CFG, P, P, P, P, P, P, P, P, P, P, P, P, P]),
+        "moe_mx_quantize": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, P, P, P,
+                                           P]),
+        "moe_mx_dequantize": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, P, P, P,
+                                             P]),
+        "moe_add_rmsnorm": (ctypes.c_int, [CFG, P, P, P, ctypes.c_float, P, P, ctypes.c_int32, P, P, P]),
+        "moe_expert_up_mx": (ctypes.c_int, [CFG, ctypes.c_int32, P, P, P, P, P, P, P, P, P]),
+        "moe_expert_down_mx": (ctypes.c_int, [CFG, ctypes.c_int32, P, P, P, P, P, P, P]),
+        "moe_expert_ffn_mx": (ctypes.c_int, [CFG, ctypes.c_int32, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        "moe_forward_mx": (ctypes.c_int, [CFG, ctypes.c_int32, P, P, P, ctypes.c_float, P, P, P, P, P, P, P, P, P, P,
+                                          P, P, P, P, P, ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -373,3 +389,140 @@ def moe_forward_noalloc(cfg, X, Wg, gate_bias, W1, W2, out, topk_ids, topk_w, ex
                                                           _ptr(W1), _ptr(W2), _ptr(out), _ptr(topk_ids),
                                                           _ptr(topk_w), _ptr(expert_counts), _ptr(expert_offsets),
                                                           _ptr(perm), _ptr(inv_perm), _stream(stream)))
+
+
+# ---- microscaled (MX) operands
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _mx_args(fn, args) -> None:
+    """Check buffers as _arg does (args: (name, buffer, dtypes, elements)), and that
+    each lives on the current device: the kernels run on a stream of that
+    device."""
+    for name, t, dtypes, numel in args:
+        _arg(fn, name, t, None, numel)
+        if not isinstance(t, torch.Tensor) or numel <= 0:
+            continue
+        dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+        if t.dtype not in dtypes:
+            raise TypeError(f"{fn}: {name} must have dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _mx(name, codes, scales, fmt, rows, cols):
+    """The two checks of one microscaled array [rows, cols]."""
+    n = max(rows, 0) * max(cols, 0)
+    return ((name + " codes", codes, _CODES if fmt == MOE_MXFP8 else torch.uint8, n if fmt == MOE_MXFP8 else n // 2),
+            (name + " scales", scales, _SCALES, n // 32))
+
+
+def _ws_bytes(ws, ws_bytes):
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    return int(ws_bytes)
+
+
+def _ws_arg(ws, ws_bytes):
+    """The check of a workspace: its kind and place, and that it holds the ws_bytes it is said to hold (whether
+    they are enough the library says)."""
+    if not isinstance(ws, torch.Tensor):
+        return ("ws", ws, torch.uint8, 1)
+    n = ws.numel() if ws_bytes is None else -(-int(ws_bytes) // ws.element_size())
+    return ("ws", ws, ws.dtype, n)
+
+
+def _any_dtype(dtype):
+    return torch.bfloat16 if dtype == MOE_BF16 else torch.float32
+
+
+def moe_mx_quantize(dtype, fmt, rows, cols, X, codes, scales, stream=None) -> None:
+    """X [rows, cols] (dtype MOE_BF16 or MOE_F32) to MX codes and scales (fmt MOE_MXFP4 or MOE_MXFP8)."""
+    _mx_args("moe_mx_quantize", (("X", X, _any_dtype(dtype), max(rows, 0) * max(cols, 0)),
+                                 *_mx("X's", codes, scales, fmt, rows, cols)))
+    _check("moe_mx_quantize", LIB.moe_mx_quantize(int(dtype), int(fmt), int(rows), int(cols), _ptr(X), _ptr(codes),
+                                                  _ptr(scales), _stream(stream)))
+
+
+def moe_mx_dequantize(dtype, fmt, rows, cols, codes, scales, X, stream=None) -> None:
+    """MX codes and scales to X [rows, cols]."""
+    _mx_args("moe_mx_dequantize", (*_mx("X's", codes, scales, fmt, rows, cols),
+                                   ("X", X, _any_dtype(dtype), max(rows, 0) * max(cols, 0))))
+    _check("moe_mx_dequantize", LIB.moe_mx_dequantize(int(dtype), int(fmt), int(rows), int(cols), _ptr(codes),
+                                                      _ptr(scales), _ptr(X), _stream(stream)))
+
+
+def moe_add_rmsnorm(cfg, X, residual, gamma, eps, sum, y, fmt=MOE_MXFP8, codes=None, scales=None,
+                    stream=None) -> None:
+    """sum = X + residual, y = rmsnorm(sum) * gamma and its MX form; residual, sum, y, codes with scales may be None."""
+    T, d, F, E, k, Tk = _dims(cfg)
+    dt = _layer_dtype(cfg)
+    _mx_args("moe_add_rmsnorm", (("X", X, dt, T * d), ("residual", residual, dt, T * d), ("gamma", gamma, dt, d * (T > 0)),
+                                 ("sum", sum, dt, T * d), ("y", y, dt, T * d), *_mx("y's", codes, scales, fmt, T, d)))
+    _check("moe_add_rmsnorm", LIB.moe_add_rmsnorm(ctypes.byref(cfg), _ptr(X), _ptr(residual), _ptr(gamma), float(eps),
+                                                  _ptr(sum), _ptr(y), int(fmt), _ptr(codes), _ptr(scales),
+                                                  _stream(stream)))
+
+
+def _mx_up(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s):
+    T, d, F, E, k, Tk = _dims(cfg)
+    some = T > 0
+    return (*_mx("X's", Xq, Xs, fmt, T, d), ("perm", perm, torch.int32, Tk),
+            ("expert_offsets", expert_offsets, torch.int32, (E + 1) * some),
+            *_mx("W1's", W1q, W1s, MOE_MXFP4, E * F * some, d))
+
+
+def moe_expert_up_mx(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s, Hq, Hs, stream=None) -> None:
+    T, d, F, E, k, Tk = _dims(cfg)
+    _mx_args("moe_expert_up_mx", (*_mx_up(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s),
+                                  *_mx("H's", Hq, Hs, fmt, Tk, F)))
+    _check("moe_expert_up_mx", LIB.moe_expert_up_mx(ctypes.byref(cfg), int(fmt), _ptr(Xq), _ptr(Xs), _ptr(perm),
+                                                    _ptr(expert_offsets), _ptr(W1q), _ptr(W1s), _ptr(Hq), _ptr(Hs),
+                                                    _stream(stream)))
+
+
+def moe_expert_down_mx(cfg, fmt, Hq, Hs, expert_offsets, W2q, W2s, Yp, stream=None) -> None:
+    T, d, F, E, k, Tk = _dims(cfg)
+    some = T > 0
+    _mx_args("moe_expert_down_mx", (*_mx("H's", Hq, Hs, fmt, Tk, F),
+                                    ("expert_offsets", expert_offsets, torch.int32, (E + 1) * some),
+                                    *_mx("W2's", W2q, W2s, MOE_MXFP4, E * d * some, F),
+                                    ("Yp", Yp, _layer_dtype(cfg), Tk * d)))
+    _check("moe_expert_down_mx", LIB.moe_expert_down_mx(ctypes.byref(cfg), int(fmt), _ptr(Hq), _ptr(Hs),
+                                                        _ptr(expert_offsets), _ptr(W2q), _ptr(W2s), _ptr(Yp),
+                                                        _stream(stream)))
+
+
+def moe_expert_ffn_mx(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s, W2q, W2s, Yp, ws, ws_bytes=None,
+                      stream=None) -> None:
+    T, d, F, E, k, Tk = _dims(cfg)
+    _mx_args("moe_expert_ffn_mx", (*_mx_up(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s),
+                                   *_mx("W2's", W2q, W2s, MOE_MXFP4, E * d * (T > 0), F),
+                                   ("Yp", Yp, _layer_dtype(cfg), Tk * d), _ws_arg(ws, ws_bytes)))
+    _check("moe_expert_ffn_mx", LIB.moe_expert_ffn_mx(ctypes.byref(cfg), int(fmt), _ptr(Xq), _ptr(Xs), _ptr(perm),
+                                                      _ptr(expert_offsets), _ptr(W1q), _ptr(W1s), _ptr(W2q),
+                                                      _ptr(W2s), _ptr(Yp), _ptr(ws), _ws_bytes(ws, ws_bytes),
+                                                      _stream(stream)))
+
+
+def moe_forward_mx(cfg, fmt, X, residual, gamma, eps, Wg, gate_bias, W1q, W1s, W2q, W2s, sum, out, topk_ids, topk_w,
+                   expert_counts, expert_offsets, perm, inv_perm, ws, ws_bytes=None, stream=None) -> None:
+    T, d, F, E, k, Tk = _dims(cfg)
+    dt = _layer_dtype(cfg)
+    some = T > 0
+    _mx_args("moe_forward_mx", (("X", X, dt, T * d), ("residual", residual, dt, T * d), ("gamma", gamma, dt, d * some),
+                                ("Wg", Wg, dt, d * E * some), ("gate_bias", gate_bias, torch.float32, E * some),
+                                *_mx("W1's", W1q, W1s, MOE_MXFP4, E * F * some, d),
+                                *_mx("W2's", W2q, W2s, MOE_MXFP4, E * d * some, F),
+                                ("sum", sum, dt, T * d), ("out", out, dt, T * d), ("topk_ids", topk_ids, torch.int32, Tk),
+                                ("topk_w", topk_w, torch.float32, Tk), ("expert_counts", expert_counts, torch.int32, E),
+                                ("expert_offsets", expert_offsets, torch.int32, E + 1),
+                                ("perm", perm, torch.int32, Tk), ("inv_perm", inv_perm, torch.int32, Tk),
+                                _ws_arg(ws, ws_bytes)))
+    _check("moe_forward_mx", LIB.moe_forward_mx(ctypes.byref(cfg), int(fmt), _ptr(X), _ptr(residual), _ptr(gamma),
+                                                float(eps), _ptr(Wg), _ptr(gate_bias), _ptr(W1q), _ptr(W1s),
+                                                _ptr(W2q), _ptr(W2s), _ptr(sum), _ptr(out), _ptr(topk_ids),
+                                                _ptr(topk_w), _ptr(expert_counts), _ptr(expert_offsets), _ptr(perm),
+                                                _ptr(inv_perm), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))

@@ -87,9 +87,70 @@ bool gathers(const moe_config* c) {
                                    c->num_tokens, static_cast<int>(pairs_of(c)), c->num_experts);
 }
 
+// Bytes of the MX codes (8 bits, the wider format) and scales of rows x cols elements.
+size_t mx_bytes(size_t rows, size_t cols) { return align256(rows * cols) + align256(rows * (cols / 32)); }
+size_t ffn_mx_bytes(const moe_config* c) { return mx_bytes(pairs_of(c), c->intermediate_size); }
+size_t forward_mx_bytes(const moe_config* c) {
+  const size_t t = static_cast<size_t>(c->num_tokens);
+  return align256(route_bytes(c)) + align256(dispatch_bytes(c)) + align256(t * c->hidden_size * esize(c)) +
+         mx_bytes(t, c->hidden_size) + ffn_mx_bytes(c) + xp_bytes(c);
+}
+
+bool valid_format(int32_t f) { return f == MOE_MXFP4 || f == MOE_MXFP8; }
+
+// The MX kernels load and store 16 bytes at a time (null passes: checked apart).
+template <typename... P> bool aligned16(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) % 16 == 0) && ...);
+}
+
+moe_status check_mx(int32_t dtype, int32_t format, int64_t rows, int64_t cols) {
+  if ((dtype != MOE_F32 && dtype != MOE_BF16) || !valid_format(format) || rows < 0 || cols < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (cols % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && cols > (int64_t{1} << 60) / rows) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe::MxOperands mx_operands(const moe_config* c, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
+                            const int32_t* offsets, int N, int K) {
+  return moe::MxOperands{static_cast<const uint8_t*>(xq), xs, static_cast<const uint8_t*>(wq), ws, offsets,
+                         c->num_experts, N, K, static_cast<int>(pairs_of(c)), rows_per_expert_bound(c)};
+}
+
 moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
+
+// The router and the dispatch of a forward; Xp_out may be null (indices only).
+moe_status route_and_dispatch(const moe_config* cfg, const void* X, const void* Wg, const float* gate_bias,
+                              int32_t* topk_ids, float* topk_w, int32_t* expert_counts, int32_t* expert_offsets,
+                              int32_t* perm, int32_t* inv_perm, void* Xp_out, void* rws, void* dws, void* stream) {
+  const moe::RouterSplit split =
+      moe::router_split(cfg->num_tokens, cfg->hidden_size, cfg->num_experts, cfg->dtype, rws);
+  if (split.partial != nullptr && moe::dispatch_is_single_block(cfg->num_tokens, cfg->num_experts_per_tok)) {
+    // Small batch with a K-split router: the router writes its partial
+    // logits only, and one block selects and dispatches (one launch fewer,
+    // same results as moe_route followed by moe_dispatch).
+    if (hipError_t e = moe::launch_router(cfg->dtype, X, Wg, gate_bias, cfg->num_tokens, cfg->hidden_size,
+                                          cfg->num_experts, cfg->num_experts_per_tok, topk_ids, topk_w, rws,
+                                          as_stream(stream), /*select=*/false);
+        e != hipSuccess)
+      return MOE_ERR_HIP;
+    if (hipError_t e = moe::launch_topk_dispatch_small(
+            cfg->dtype, split.partial, split.nsplit, gate_bias, topk_ids, topk_w, X, cfg->num_tokens,
+            cfg->hidden_size, cfg->num_experts, cfg->num_experts_per_tok, cfg->expert_capacity, expert_counts,
+            expert_offsets, perm, inv_perm, Xp_out, as_stream(stream));
+        e != hipSuccess)
+      return MOE_ERR_HIP;
+  } else {
+    if (moe_status s = moe_route(cfg, X, Wg, gate_bias, topk_ids, topk_w, rws, route_bytes(cfg), stream);
+        s != MOE_OK)
+      return s;
+    return moe_dispatch(cfg, topk_ids, X, expert_counts, expert_offsets, perm, inv_perm, Xp_out, dws,
+                        dispatch_bytes(cfg), stream);
+  }
+  return MOE_OK;
+}
 
 }  // namespace
 
@@ -143,6 +204,8 @@ moe_status moe_workspace_size(const moe_config* cfg, int32_t op, size_t* bytes) 
     case MOE_OP_FORWARD_REROUTE:
       *bytes = align256(route_bytes(cfg)) + align256(dispatch_reroute_bytes(cfg)) + 2 * xp_bytes(cfg) + h_bytes(cfg);
       return MOE_OK;
+    case MOE_OP_EXPERT_FFN_MX: *bytes = ffn_mx_bytes(cfg); return MOE_OK;
+    case MOE_OP_FORWARD_MX: *bytes = forward_mx_bytes(cfg); return MOE_OK;
     default: return MOE_ERR_INVALID_ARG;
   }
 }
@@ -316,36 +379,14 @@ moe_status moe_forward(const moe_config* cfg, const void* X, const void* Wg, con
   void* H = p;
   p += h_bytes(cfg);
   void* Yp = p;
-  const moe::RouterSplit split =
-      moe::router_split(cfg->num_tokens, cfg->hidden_size, cfg->num_experts, cfg->dtype, rws);
   // Where the up-projection can read each pair's token row from X through
   // perm, the dispatch writes indices only.
   const bool gather = gathers(cfg);
   void* const Xp_out = gather ? nullptr : Xp;
-  if (split.partial != nullptr && moe::dispatch_is_single_block(cfg->num_tokens, cfg->num_experts_per_tok)) {
-    // Small batch with a K-split router: the router writes its partial
-    // logits only, and one block selects and dispatches (one launch fewer,
-    // same results as moe_route followed by moe_dispatch).
-    if (hipError_t e = moe::launch_router(cfg->dtype, X, Wg, gate_bias, cfg->num_tokens, cfg->hidden_size,
-                                          cfg->num_experts, cfg->num_experts_per_tok, topk_ids, topk_w, rws,
-                                          as_stream(stream), /*select=*/false);
-        e != hipSuccess)
-      return MOE_ERR_HIP;
-    if (hipError_t e = moe::launch_topk_dispatch_small(
-            cfg->dtype, split.partial, split.nsplit, gate_bias, topk_ids, topk_w, X, cfg->num_tokens,
-            cfg->hidden_size, cfg->num_experts, cfg->num_experts_per_tok, cfg->expert_capacity, expert_counts,
-            expert_offsets, perm, inv_perm, Xp_out, as_stream(stream));
-        e != hipSuccess)
-      return MOE_ERR_HIP;
-  } else {
-    if (moe_status s = moe_route(cfg, X, Wg, gate_bias, topk_ids, topk_w, rws, route_bytes(cfg), stream);
-        s != MOE_OK)
-      return s;
-    if (moe_status s = moe_dispatch(cfg, topk_ids, X, expert_counts, expert_offsets, perm, inv_perm, Xp_out, dws,
-                                    dispatch_bytes(cfg), stream);
-        s != MOE_OK)
-      return s;
-  }
+  if (moe_status s = route_and_dispatch(cfg, X, Wg, gate_bias, topk_ids, topk_w, expert_counts, expert_offsets, perm,
+                                        inv_perm, Xp_out, rws, dws, stream);
+      s != MOE_OK)
+    return s;
   if (cfg->num_tokens == 0) return MOE_OK;
   if (moe_status s = gather ? moe_expert_up_gather(cfg, X, perm, expert_offsets, W1, H, stream)
                             : moe_expert_up(cfg, Xp, expert_offsets, W1, H, stream);
@@ -393,6 +434,122 @@ moe_status moe_forward_reroute(const moe_config* cfg, const void* X, const void*
       s != MOE_OK)
     return s;
   if (moe_status s = moe_expert_down(cfg, H, expert_offsets, W2, Yp, stream); s != MOE_OK) return s;
+  return moe_combine(cfg, Yp, inv_perm, topk_w, out, stream);
+}
+
+moe_status moe_mx_quantize(int32_t dtype, int32_t format, int64_t rows, int64_t cols, const void* X, void* codes,
+                           uint8_t* scales, void* stream) {
+  if (moe_status s = check_mx(dtype, format, rows, cols); s != MOE_OK) return s;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!X || !codes || !scales || !aligned16(X, codes, scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_mx_quantize(dtype, format, X, codes, scales, rows * cols, as_stream(stream)));
+}
+
+moe_status moe_mx_dequantize(int32_t dtype, int32_t format, int64_t rows, int64_t cols, const void* codes,
+                             const uint8_t* scales, void* X, void* stream) {
+  if (moe_status s = check_mx(dtype, format, rows, cols); s != MOE_OK) return s;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!X || !codes || !scales || !aligned16(X, codes, scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_mx_dequantize(dtype, format, codes, scales, X, rows * cols, as_stream(stream)));
+}
+
+moe_status moe_add_rmsnorm(const moe_config* cfg, const void* X, const void* residual, const void* gamma, float eps,
+                           void* sum, void* y, int32_t format, void* codes, uint8_t* scales, void* stream) {
+  if (moe_status s = check_cfg(cfg); s != MOE_OK) return s;
+  if (!valid_format(format) || !(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (cfg->hidden_size > moe::kNormMaxHidden) return MOE_ERR_UNSUPPORTED;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if (!X || !gamma || (codes == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((!sum && !y && !codes) || (sum != nullptr && sum == y)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(X, residual, gamma, sum, y, codes, scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_add_rmsnorm(cfg->dtype, format, X, residual, gamma, eps, sum, y, codes, scales,
+                                            cfg->num_tokens, cfg->hidden_size, as_stream(stream)));
+}
+
+moe_status moe_expert_up_mx(const moe_config* cfg, int32_t format, const void* Xq, const uint8_t* Xs,
+                            const int32_t* perm, const int32_t* expert_offsets, const void* W1q, const uint8_t* W1s,
+                            void* Hq, uint8_t* Hs, void* stream) {
+  if (moe_status s = check_cfg(cfg); s != MOE_OK) return s;
+  if (!valid_format(format)) return MOE_ERR_INVALID_ARG;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if (!Xq || !Xs || !perm || !expert_offsets || !W1q || !W1s || !Hq || !Hs) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(Xq, Xs, W1q, W1s, Hq, Hs)) return MOE_ERR_INVALID_ARG;
+  const moe::MxOperands o =
+      mx_operands(cfg, Xq, Xs, W1q, W1s, expert_offsets, cfg->intermediate_size, cfg->hidden_size);
+  return hip_status(moe::launch_mx_up(format, o, perm, cfg->num_experts_per_tok, cfg->num_tokens,
+                                      static_cast<uint8_t*>(Hq), Hs, as_stream(stream)));
+}
+
+moe_status moe_expert_down_mx(const moe_config* cfg, int32_t format, const void* Hq, const uint8_t* Hs,
+                              const int32_t* expert_offsets, const void* W2q, const uint8_t* W2s, void* Yp,
+                              void* stream) {
+  if (moe_status s = check_cfg(cfg); s != MOE_OK) return s;
+  if (!valid_format(format)) return MOE_ERR_INVALID_ARG;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if (!Hq || !Hs || !expert_offsets || !W2q || !W2s || !Yp) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(Hq, Hs, W2q, W2s, Yp)) return MOE_ERR_INVALID_ARG;
+  const moe::MxOperands o =
+      mx_operands(cfg, Hq, Hs, W2q, W2s, expert_offsets, cfg->hidden_size, cfg->intermediate_size);
+  return hip_status(moe::launch_mx_down(cfg->dtype, format, o, Yp, as_stream(stream)));
+}
+
+moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t format, const void* Xq, const uint8_t* Xs,
+                             const int32_t* perm, const int32_t* expert_offsets, const void* W1q, const uint8_t* W1s,
+                             const void* W2q, const uint8_t* W2s, void* Yp, void* ws, size_t ws_bytes, void* stream) {
+  if (moe_status s = check_cfg(cfg); s != MOE_OK) return s;
+  if (!valid_format(format)) return MOE_ERR_INVALID_ARG;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if (!Xq || !Xs || !perm || !expert_offsets || !W1q || !W1s || !W2q || !W2s || !Yp) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < ffn_mx_bytes(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  // every operand of both products, so that a refused call has enqueued nothing
+  if (ws == nullptr || !aligned16(Xq, Xs, W1q, W1s, W2q, W2s, Yp, ws)) return MOE_ERR_INVALID_ARG;
+  uint8_t* Hq = static_cast<uint8_t*>(ws);
+  uint8_t* Hs = Hq + align256(pairs_of(cfg) * cfg->intermediate_size);
+  if (moe_status s = moe_expert_up_mx(cfg, format, Xq, Xs, perm, expert_offsets, W1q, W1s, Hq, Hs, stream);
+      s != MOE_OK)
+    return s;
+  return moe_expert_down_mx(cfg, format, Hq, Hs, expert_offsets, W2q, W2s, Yp, stream);
+}
+
+moe_status moe_forward_mx(const moe_config* cfg, int32_t format, const void* X, const void* residual,
+                          const void* gamma, float eps, const void* Wg, const float* gate_bias, const void* W1q,
+                          const uint8_t* W1s, const void* W2q, const uint8_t* W2s, void* sum, void* out,
+                          int32_t* topk_ids, float* topk_w, int32_t* expert_counts, int32_t* expert_offsets,
+                          int32_t* perm, int32_t* inv_perm, void* ws, size_t ws_bytes, void* stream) {
+  if (moe_status s = check_cfg(cfg); s != MOE_OK) return s;
+  if (!valid_format(format) || !(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (cfg->hidden_size > moe::kNormMaxHidden) return MOE_ERR_UNSUPPORTED;
+  if (!expert_counts || !expert_offsets) return MOE_ERR_INVALID_ARG;
+  if (cfg->num_tokens > 0 && (!X || !gamma || !Wg || !W1q || !W1s || !W2q || !W2s || !out || !topk_ids || !topk_w ||
+                              !perm || !inv_perm))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < forward_mx_bytes(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws == nullptr || !aligned16(X, residual, gamma, W1q, W1s, W2q, W2s, sum, out, ws)) return MOE_ERR_INVALID_ARG;
+  const size_t t = static_cast<size_t>(cfg->num_tokens);
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  auto take = [&p](size_t bytes) {
+    uint8_t* at = p;
+    p += align256(bytes);
+    return at;
+  };
+  void* rws = take(route_bytes(cfg));
+  void* dws = take(dispatch_bytes(cfg));
+  void* y = take(t * cfg->hidden_size * esize(cfg));
+  uint8_t* Xq = take(t * cfg->hidden_size);
+  uint8_t* Xs = take(t * (cfg->hidden_size / 32));
+  uint8_t* Yp = take(xp_bytes(cfg));
+  uint8_t* h = take(ffn_mx_bytes(cfg));
+  if (moe_status s = moe_add_rmsnorm(cfg, X, residual, gamma, eps, sum, y, format, Xq, Xs, stream); s != MOE_OK)
+    return s;
+  if (moe_status s = route_and_dispatch(cfg, y, Wg, gate_bias, topk_ids, topk_w, expert_counts, expert_offsets, perm,
+                                        inv_perm, nullptr, rws, dws, stream);
+      s != MOE_OK)
+    return s;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if (moe_status s = moe_expert_ffn_mx(cfg, format, Xq, Xs, perm, expert_offsets, W1q, W1s, W2q, W2s, Yp, h,
+                                       ffn_mx_bytes(cfg), stream);
+      s != MOE_OK)
+    return s;
   return moe_combine(cfg, Yp, inv_perm, topk_w, out, stream);
 }
 

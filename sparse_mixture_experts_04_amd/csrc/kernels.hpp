@@ -107,6 +107,38 @@ hipError_t launch_grouped_gemm_gather(bool gelu, const void* X, int src_rows, co
 hipError_t launch_combine(int dtype, const void* Yp, const int32_t* inv_perm, const float* topk_w, void* out, int T,
                           int d, int k, hipStream_t stream);
 
+// Quantisation of n elements (a multiple of 32) to MX codes and scales, and
+// back.  fmt: 0 = e2m1 (4 bits), 1 = e4m3 (8 bits).
+hipError_t launch_mx_quantize(int dtype, int fmt, const void* x, void* codes, uint8_t* scales, int64_t n,
+                              hipStream_t stream);
+hipError_t launch_mx_dequantize(int dtype, int fmt, const void* codes, const uint8_t* scales, void* x, int64_t n,
+                                hipStream_t stream);
+
+// sum = x + r, y = rmsnorm(x + r) * gamma and its MX form; r, sum, y and
+// codes (with scales) may be null.  d is a multiple of 64, at most
+// kNormMaxHidden.
+constexpr int kNormMaxHidden = 32768;
+hipError_t launch_add_rmsnorm(int dtype, int fmt, const void* x, const void* r, const void* gamma, float eps,
+                              void* sum, void* y, void* codes, uint8_t* scales, int T_tok, int d, hipStream_t stream);
+
+// The experts' products on MX operands.  Up: H = MX(gelu(W1 x)) for every
+// dispatched row, the row's token read through perm (row r is X row
+// gidx[r] / gdiv).  Down: Y = W2 H in dtype, H in expert order.  fmt is X's
+// and H's format; weights are e2m1.  N and K are multiples of 64.
+struct MxOperands {
+  const uint8_t* xq;   // token rows' codes and scales
+  const uint8_t* xs;
+  const uint8_t* wq;   // weights' codes and scales, [E, N, K]
+  const uint8_t* ws;
+  const int32_t* offsets;
+  int E, N, K;
+  int max_rows;        // pairs the expert-ordered side can hold
+  int rows_bound;      // rows one expert holds at most (picks the kernel; any count is computed)
+};
+hipError_t launch_mx_up(int fmt, const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, uint8_t* hq,
+                        uint8_t* hs, hipStream_t stream);
+hipError_t launch_mx_down(int dtype, int fmt, const MxOperands& o, void* y, hipStream_t stream);
+
 int device_cu_count();
 
 }  // namespace moe

@@ -1,0 +1,203 @@
+// Quantisation to the microscaled (MX) formats and back, and the residual's
+// addition with the root-mean-square norm that stands before the layer, with
+// its outputs for the router (the layer's type) and for the experts (MX).
+//
+// Quantisation (OCP Microscaling Formats v1.0): for a block of 32 consecutive
+// elements, amax = max |v|, scale 2^(floor(log2 amax) - emax), codes = v /
+// scale rounded to nearest even and saturated.  Every step is exact but that
+// one rounding, so codes and scales are the definition's, bit for bit.
+// All three kernels are bound by memory: each element is touched once, with
+// 16-byte loads, and the four lanes of a block exchange their maxima in
+// registers.
+#include "kernels.hpp"
+#include "mx.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kQThreads = 256;
+
+// A block of 32 may not straddle rows (cols is a multiple of 32), so rows
+// and columns do not matter: chunk c holds elements 8c .. 8c+7 and blocks are
+// groups of 4 chunks.
+template <typename T, int kFmt>
+__global__ __launch_bounds__(kQThreads) void mx_quantize_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
+                                                                uint8_t* __restrict__ scales, int64_t chunks) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kQThreads;
+  // chunks is a multiple of 4: the lanes of a block leave the loop together
+  for (int64_t c = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; c < chunks; c += stride) {
+    float v[8];
+    load8(x + c * 8, v);
+    const uint32_t b = mx_scale_byte<kFmt>(mx_block_max(v));
+    mx_store8<kFmt>(codes, c * 8, v, mx_inv_scale(b), b == 255u);
+    if ((c & 3) == 0) scales[c >> 2] = static_cast<uint8_t>(b);
+  }
+}
+
+template <typename T, int kFmt>
+__global__ __launch_bounds__(kQThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                                  const uint8_t* __restrict__ scales,
+                                                                  T* __restrict__ x, int64_t chunks) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kQThreads;
+  for (int64_t c = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; c < chunks; c += stride) {
+    float v[8];
+    mx_load8<kFmt>(codes, c * 8, v);
+    const float s = mx_scale(scales[c >> 2]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s;
+    store8(x + c * 8, v);
+  }
+}
+
+int quant_grid(int64_t chunks) {
+  const int64_t blocks = (chunks + kQThreads - 1) / kQThreads;
+  const int64_t cap = static_cast<int64_t>(device_cu_count()) * 16;
+  return static_cast<int>(blocks < cap ? blocks : cap);
+}
+
+template <typename T>
+hipError_t quantize_t(int fmt, const void* x, uint8_t* codes, uint8_t* scales, int64_t chunks, hipStream_t stream) {
+  const dim3 grid(quant_grid(chunks));
+  if (fmt == kMxFp4)
+    hipLaunchKernelGGL((mx_quantize_kernel<T, kMxFp4>), grid, dim3(kQThreads), 0, stream, static_cast<const T*>(x),
+                       codes, scales, chunks);
+  else
+    hipLaunchKernelGGL((mx_quantize_kernel<T, kMxFp8>), grid, dim3(kQThreads), 0, stream, static_cast<const T*>(x),
+                       codes, scales, chunks);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dequantize_t(int fmt, const uint8_t* codes, const uint8_t* scales, void* x, int64_t chunks,
+                        hipStream_t stream) {
+  const dim3 grid(quant_grid(chunks));
+  if (fmt == kMxFp4)
+    hipLaunchKernelGGL((mx_dequantize_kernel<T, kMxFp4>), grid, dim3(kQThreads), 0, stream, codes, scales,
+                       static_cast<T*>(x), chunks);
+  else
+    hipLaunchKernelGGL((mx_dequantize_kernel<T, kMxFp8>), grid, dim3(kQThreads), 0, stream, codes, scales,
+                       static_cast<T*>(x), chunks);
+  return hipGetLastError();
+}
+
+// One block per token.  s = x + r is formed in fp32 and kept in registers
+// (kNC chunks of 8 elements per thread), so each input is read once.
+//   sum = round(s);  n = s * rstd * gamma;  y = round(n);  MX codes of n
+// The norm and the codes start from the unrounded s and n: the only roundings
+// are the ones of the stored results.  The squares are summed in fp64: fp32
+// would overflow to infinity for |s| past 1.8e19, which bf16 holds.
+// x, r, sum and y may be the same buffer: a thread reads its elements of x and
+// r before it writes them anywhere, and nobody else reads them.
+template <typename T, int kFmt, int kNC, int kThreads>
+__global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(const T* x, const T* r, const T* __restrict__ gamma,
+                                                               float eps, T* sum, T* y, uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ scales, int d) {
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int chunks = d / 8;
+  const int64_t base = t * d;
+  float v[kNC][8];
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+    const int c = tid + i * kThreads;
+    if (c < chunks) {
+      load8(x + base + c * 8, v[i]);
+      if (r != nullptr) {
+        float w[8];
+        load8(r + base + c * 8, w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[i][q] += w[q];
+      }
+      if (sum != nullptr) store8(sum + base + c * 8, v[i]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) ss = fma(static_cast<double>(v[i][q]), static_cast<double>(v[i][q]), ss);
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) ss += __shfl_xor(ss, m);
+  if constexpr (kThreads > kWave) {
+    __shared__ double part[kThreads / kWave];
+    if (tid % kWave == 0) part[tid / kWave] = ss;
+    __syncthreads();
+    ss = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) ss += part[w];
+  }
+  const float rstd = static_cast<float>(1.0 / sqrt(ss / d + static_cast<double>(eps)));
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+    const int c = tid + i * kThreads;
+    if (c < chunks) {  // chunks is a multiple of 8: the 4 lanes of a block are in or out together
+      float g[8];
+      load8(gamma + c * 8, g);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * rstd * g[q];
+      if (y != nullptr) store8(y + base + c * 8, v[i]);
+      if (codes != nullptr) {
+        const uint32_t b = mx_scale_byte<kFmt>(mx_block_max(v[i]));
+        mx_store8<kFmt>(codes, base + c * 8, v[i], mx_inv_scale(b), b == 255u);
+        if ((c & 3) == 0) scales[(base >> 5) + (c >> 2)] = static_cast<uint8_t>(b);
+      }
+    }
+  }
+}
+
+template <typename T, int kFmt>
+hipError_t rmsnorm_tf(const T* x, const T* r, const T* gamma, float eps, T* sum, T* y, uint8_t* codes,
+                      uint8_t* scales, int T_tok, int d, hipStream_t stream) {
+  const int chunks = d / 8;
+#define MOE_NORM(NC, TH)                                                                                             \
+  hipLaunchKernelGGL((add_rmsnorm_kernel<T, kFmt, NC, TH>), dim3(T_tok), dim3(TH), 0, stream, x, r, gamma, eps, sum, \
+                     y, codes, scales, d)
+  if (chunks <= 64) MOE_NORM(1, 64);
+  else if (chunks <= 256) MOE_NORM(1, 256);
+  else if (chunks <= 512) MOE_NORM(2, 256);
+  else if (chunks <= 1024) MOE_NORM(4, 256);
+  else if (chunks <= 4096) MOE_NORM(4, 1024);
+  else return hipErrorInvalidValue;
+#undef MOE_NORM
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t rmsnorm_t(int fmt, const void* x, const void* r, const void* gamma, float eps, void* sum, void* y,
+                     uint8_t* codes, uint8_t* scales, int T_tok, int d, hipStream_t stream) {
+  const T* xp = static_cast<const T*>(x);
+  const T* rp = static_cast<const T*>(r);
+  const T* gp = static_cast<const T*>(gamma);
+  return fmt == kMxFp4
+             ? rmsnorm_tf<T, kMxFp4>(xp, rp, gp, eps, static_cast<T*>(sum), static_cast<T*>(y), codes, scales, T_tok,
+                                     d, stream)
+             : rmsnorm_tf<T, kMxFp8>(xp, rp, gp, eps, static_cast<T*>(sum), static_cast<T*>(y), codes, scales, T_tok,
+                                     d, stream);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(int dtype, int fmt, const void* x, void* codes, uint8_t* scales, int64_t n,
+                              hipStream_t stream) {
+  if (n <= 0) return hipSuccess;
+  uint8_t* c = static_cast<uint8_t*>(codes);
+  return dtype == kDtypeBF16 ? quantize_t<uint16_t>(fmt, x, c, scales, n / 8, stream)
+                             : quantize_t<float>(fmt, x, c, scales, n / 8, stream);
+}
+
+hipError_t launch_mx_dequantize(int dtype, int fmt, const void* codes, const uint8_t* scales, void* x, int64_t n,
+                                hipStream_t stream) {
+  if (n <= 0) return hipSuccess;
+  const uint8_t* c = static_cast<const uint8_t*>(codes);
+  return dtype == kDtypeBF16 ? dequantize_t<uint16_t>(fmt, c, scales, x, n / 8, stream)
+                             : dequantize_t<float>(fmt, c, scales, x, n / 8, stream);
+}
+
+hipError_t launch_add_rmsnorm(int dtype, int fmt, const void* x, const void* r, const void* gamma, float eps,
+                              void* sum, void* y, void* codes, uint8_t* scales, int T_tok, int d,
+                              hipStream_t stream) {
+  if (T_tok <= 0) return hipSuccess;
+  uint8_t* c = static_cast<uint8_t*>(codes);
+  return dtype == kDtypeBF16 ? rmsnorm_t<uint16_t>(fmt, x, r, gamma, eps, sum, y, c, scales, T_tok, d, stream)
+                             : rmsnorm_t<float>(fmt, x, r, gamma, eps, sum, y, c, scales, T_tok, d, stream);
+}
+
+}  // namespace moe
