@@ -398,18 +398,26 @@ _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 
 
 def _mx_args(fn, args) -> None:
-    """Check buffers as _arg does (args: (name, buffer, dtypes, elements)), and that
+    """Check buffers as _arg does (args: (name, buffer, dtype or dtypes, elements)), and that
     each lives on the current device: the kernels run on a stream of that
     device."""
-    for name, t, dtypes, numel in args:
-        _arg(fn, name, t, None, numel)
-        if not isinstance(t, torch.Tensor) or numel <= 0:
+    device = None
+    for name, t, dtype, numel in args:
+        if t is None or numel <= 0 or type(t) is int:
             continue
-        dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-        if t.dtype not in dtypes:
-            raise TypeError(f"{fn}: {name} must have dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if device is None:
+            device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        if (isinstance(t, torch.Tensor) and t.get_device() == device and t.numel() >= numel and t.is_contiguous()
+                and (t.dtype in dtype if type(dtype) is tuple else t.dtype is dtype)):
+            continue
+        _arg(fn, name, t, None, numel)  # names what is wrong, in _arg's words
+        if isinstance(t, torch.Tensor):
+            dtypes = dtype if type(dtype) is tuple else (dtype,)
+            if t.dtype not in dtypes:
+                raise TypeError(f"{fn}: {name} must have dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
+            if t.device.index != torch.cuda.current_device():
+                raise ValueError(f"{fn}: {name} is on {t.device}, the current device is "
+                                 f"cuda:{torch.cuda.current_device()}")
 
 
 def _mx(name, codes, scales, fmt, rows, cols):
@@ -417,6 +425,16 @@ def _mx(name, codes, scales, fmt, rows, cols):
     n = max(rows, 0) * max(cols, 0)
     return ((name + " codes", codes, _CODES if fmt == MOE_MXFP8 else torch.uint8, n if fmt == MOE_MXFP8 else n // 2),
             (name + " scales", scales, _SCALES, n // 32))
+
+
+def _mx_stream(stream):
+    """As _stream; torch's current stream without building a Stream object where this torch offers that."""
+    if stream is None and _RAW_STREAM is not None and torch.cuda.is_initialized():
+        return _RAW_STREAM(torch.cuda.current_device())
+    return _stream(stream)
+
+
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _ws_bytes(ws, ws_bytes):
@@ -443,7 +461,7 @@ def moe_mx_quantize(dtype, fmt, rows, cols, X, codes, scales, stream=None) -> No
     _mx_args("moe_mx_quantize", (("X", X, _any_dtype(dtype), max(rows, 0) * max(cols, 0)),
                                  *_mx("X's", codes, scales, fmt, rows, cols)))
     _check("moe_mx_quantize", LIB.moe_mx_quantize(int(dtype), int(fmt), int(rows), int(cols), _ptr(X), _ptr(codes),
-                                                  _ptr(scales), _stream(stream)))
+                                                  _ptr(scales), _mx_stream(stream)))
 
 
 def moe_mx_dequantize(dtype, fmt, rows, cols, codes, scales, X, stream=None) -> None:
@@ -451,7 +469,7 @@ def moe_mx_dequantize(dtype, fmt, rows, cols, codes, scales, X, stream=None) -> 
     _mx_args("moe_mx_dequantize", (*_mx("X's", codes, scales, fmt, rows, cols),
                                    ("X", X, _any_dtype(dtype), max(rows, 0) * max(cols, 0))))
     _check("moe_mx_dequantize", LIB.moe_mx_dequantize(int(dtype), int(fmt), int(rows), int(cols), _ptr(codes),
-                                                      _ptr(scales), _ptr(X), _stream(stream)))
+                                                      _ptr(scales), _ptr(X), _mx_stream(stream)))
 
 
 def moe_add_rmsnorm(cfg, X, residual, gamma, eps, sum, y, fmt=MOE_MXFP8, codes=None, scales=None,
@@ -463,7 +481,7 @@ def moe_add_rmsnorm(cfg, X, residual, gamma, eps, sum, y, fmt=MOE_MXFP8, codes=N
                                  ("sum", sum, dt, T * d), ("y", y, dt, T * d), *_mx("y's", codes, scales, fmt, T, d)))
     _check("moe_add_rmsnorm", LIB.moe_add_rmsnorm(ctypes.byref(cfg), _ptr(X), _ptr(residual), _ptr(gamma), float(eps),
                                                   _ptr(sum), _ptr(y), int(fmt), _ptr(codes), _ptr(scales),
-                                                  _stream(stream)))
+                                                  _mx_stream(stream)))
 
 
 def _mx_up(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s):
@@ -480,7 +498,7 @@ def moe_expert_up_mx(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s, Hq, Hs, s
                                   *_mx("H's", Hq, Hs, fmt, Tk, F)))
     _check("moe_expert_up_mx", LIB.moe_expert_up_mx(ctypes.byref(cfg), int(fmt), _ptr(Xq), _ptr(Xs), _ptr(perm),
                                                     _ptr(expert_offsets), _ptr(W1q), _ptr(W1s), _ptr(Hq), _ptr(Hs),
-                                                    _stream(stream)))
+                                                    _mx_stream(stream)))
 
 
 def moe_expert_down_mx(cfg, fmt, Hq, Hs, expert_offsets, W2q, W2s, Yp, stream=None) -> None:
@@ -492,7 +510,7 @@ def moe_expert_down_mx(cfg, fmt, Hq, Hs, expert_offsets, W2q, W2s, Yp, stream=No
                                     ("Yp", Yp, _layer_dtype(cfg), Tk * d)))
     _check("moe_expert_down_mx", LIB.moe_expert_down_mx(ctypes.byref(cfg), int(fmt), _ptr(Hq), _ptr(Hs),
                                                         _ptr(expert_offsets), _ptr(W2q), _ptr(W2s), _ptr(Yp),
-                                                        _stream(stream)))
+                                                        _mx_stream(stream)))
 
 
 def moe_expert_ffn_mx(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s, W2q, W2s, Yp, ws, ws_bytes=None,
@@ -504,7 +522,7 @@ def moe_expert_ffn_mx(cfg, fmt, Xq, Xs, perm, expert_offsets, W1q, W1s, W2q, W2s
     _check("moe_expert_ffn_mx", LIB.moe_expert_ffn_mx(ctypes.byref(cfg), int(fmt), _ptr(Xq), _ptr(Xs), _ptr(perm),
                                                       _ptr(expert_offsets), _ptr(W1q), _ptr(W1s), _ptr(W2q),
                                                       _ptr(W2s), _ptr(Yp), _ptr(ws), _ws_bytes(ws, ws_bytes),
-                                                      _stream(stream)))
+                                                      _mx_stream(stream)))
 
 
 def moe_forward_mx(cfg, fmt, X, residual, gamma, eps, Wg, gate_bias, W1q, W1s, W2q, W2s, sum, out, topk_ids, topk_w,
@@ -525,4 +543,4 @@ def moe_forward_mx(cfg, fmt, X, residual, gamma, eps, Wg, gate_bias, W1q, W1s, W
                                                 float(eps), _ptr(Wg), _ptr(gate_bias), _ptr(W1q), _ptr(W1s),
                                                 _ptr(W2q), _ptr(W2s), _ptr(sum), _ptr(out), _ptr(topk_ids),
                                                 _ptr(topk_w), _ptr(expert_counts), _ptr(expert_offsets), _ptr(perm),
-                                                _ptr(inv_perm), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+                                                _ptr(inv_perm), _ptr(ws), _ws_bytes(ws, ws_bytes), _mx_stream(stream)))

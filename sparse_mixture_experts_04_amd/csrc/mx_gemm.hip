@@ -53,6 +53,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, int
 template <int kFmt> struct UpOut {
   uint8_t* hq;
   uint8_t* hs;
+  // One value per lane, the block of 32 in 32 consecutive lanes: column n0 + c of row r.
+  __device__ __forceinline__ void store_one(int64_t r, int N, int n0, int c, bool ok, float v) const {
+    v = gelu_tanh_fast(v);
+    uint32_t m = abs_bits(v);
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), x)));
+    const uint32_t b = mx_scale_byte<kFmt>(m);
+    v *= mx_inv_scale(b);
+    const float next = __shfl_xor(v, 1);
+    if (!ok) return;
+    if constexpr (kFmt == kMxFp4) {
+      const uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, next, 1.0f, 0);
+      if ((c & 1) == 0) hq[(r * N + n0 + c) / 2] = b == 255u ? 0 : static_cast<uint8_t>(code);
+    } else {
+      const int code = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v), 0.f, 0, false);
+      hq[r * N + n0 + c] = b == 255u ? 0 : static_cast<uint8_t>(code);
+    }
+    if (c == 0) hs[(r * N + n0) / kMxBlock] = static_cast<uint8_t>(b);
+  }
   struct Tile {
     __amdgpu_buffer_rsrc_t codes, scales;
     int N;
@@ -97,6 +116,15 @@ template <int kFmt> struct UpOut {
 };
 template <typename T> struct DownOut {
   T* y;
+  __device__ __forceinline__ void store_one(int64_t r, int N, int n0, int c, bool ok, float v) const {
+    const float next = __shfl_xor(v, 1);
+    if (!ok) return;
+    if constexpr (sizeof(T) == 2) {
+      if ((c & 1) == 0) *reinterpret_cast<uint32_t*>(y + r * N + n0 + c) = pack_bf16x2(v, next);
+    } else {
+      y[r * N + n0 + c] = v;
+    }
+  }
   struct Tile {
     __amdgpu_buffer_rsrc_t res;
     int N;
@@ -201,6 +229,189 @@ __global__ __launch_bounds__(kWave) void mx_product_direct(MxOperands o, const i
   for (int q = 0; q < 16; ++q) v[q] = acc[q];
   const typename Out::Tile to(out, m0, rows, o.N);
   to.store_scale(frow, n0, half, to.store(frow, n0, half, v));
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per expert (decode): the product is bound by streaming each active
+// expert's weights once.  A block of four waves owns 32 weight rows (one MX
+// block of the result), its waves windows of 1024 of K in turn; every wave
+// asks for its whole window, 16 KB, before the first MFMA, so that with about
+// 16 waves on a CU 256 KB of it are on their way.
+//
+// One 16x16x128 scaled MFMA takes 8 weight rows x 2 K-slices (operand A) and 8
+// token rows x the same 2 slices (operand B); of its 16x16 results those of
+// matching slices are wanted, and a lane exchange adds the two.  So a weight
+// load reads a whole 128-byte line of each of 8 rows: lane (row, slice s, group
+// g) holds, at step t, block 8 t + 4 s + g of its window.  (For e4m3 rows an
+// MFMA's K block b lies in lanes of groups 2 (b % 2) and + 1, halves b / 2;
+// their addresses follow that.)  The scales of a row's window are 8 dwords, one
+// loaded by each of its 8 lanes, and handed round by lane exchanges.
+// The token groups of 8 are taken in turn under the window's weights, and
+// every wave keeps its partial sums in its own part of LDS; at the end they are
+// added in wave order.  A pass covers up to 64 token rows; an expert with more
+// gets further passes.
+constexpr int kFewWaves = 4;
+constexpr int kFewRows = 32;
+constexpr int kFewMaxTokens = 64;  // token rows of a pass
+constexpr int kWindowBlocks = 32;  // 1024 of K
+
+// The scales of blocks blk .. blk + 3 of a row of nblk (blk a multiple of 4).
+// kDwords: nblk is a multiple of 4, so rows are whole dwords; else nblk is
+// even.  Blocks past the row's end give 0.
+template <bool kDwords>
+__device__ __forceinline__ uint32_t scales4(const uint8_t* row, int blk, int nblk) {
+  const int at = blk < nblk ? blk : 0;
+  if constexpr (kDwords) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(row + at);
+    return blk < nblk ? v : 0u;
+  } else {
+    const int at2 = blk + 2 < nblk ? blk + 2 : 0;
+    const uint32_t lo = *reinterpret_cast<const uint16_t*>(row + at);
+    const uint32_t hi = *reinterpret_cast<const uint16_t*>(row + at2);
+    return (blk < nblk ? lo : 0u) | (blk + 2 < nblk ? hi << 16 : 0u);
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ f32x4_t mx_mfma16(u32x4_t w, u32x4_t x0, u32x4_t x1, f32x4_t c, uint32_t sw, uint32_t sx) {
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w, zero), frag(x0, x1), c, 4, mx_code<kFmt>(), 0,
+                                                          static_cast<int>(sw), 0, static_cast<int>(sx));
+}
+
+template <int kFmt, bool kGather, bool kDwords, typename Out>
+__global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o, const int32_t* __restrict__ gidx,
+                                                                   int gdiv, int src_rows, int pass, Out out) {
+  // partial sums: [wave][token of the pass][weight row]
+  extern __shared__ __attribute__((aligned(16))) float part[];
+  const int tid = threadIdx.x;
+  const int lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  int t_seg0 = 0, t_seg1 = 0;
+  if (lane < o.E) {
+    // offsets come from device memory: clamped, every access stays inside the buffers
+    t_seg0 = min(max(o.offsets[lane], 0), o.max_rows);
+    t_seg1 = min(max(o.offsets[lane + 1], t_seg0), o.max_rows);
+  }
+  // the block's expert: the (blockIdx.x / n-tiles)-th that has rows
+  const int ntn = o.N / kFewRows;
+  const int nth = blockIdx.x / ntn;
+  const bool active = t_seg1 > t_seg0;
+  const unsigned long long mask = __ballot(active);
+  const unsigned long long mine =
+      __ballot(active && __popcll(mask & ((1ull << lane) - 1)) == nth);
+  if (mine == 0) return;
+  const int e = __builtin_amdgcn_readfirstlane(__ffsll(mine) - 1);
+  const int n0 = (blockIdx.x - nth * ntn) * kFewRows;
+  const int seg0 = __builtin_amdgcn_readlane(t_seg0, e);
+  const int rows = __builtin_amdgcn_readlane(t_seg1, e) - seg0;
+
+  const int r8 = lane & 7;
+  const int slice = (lane >> 3) & 1;
+  const int g = lane >> 4;
+  const int nblk = o.K / kMxBlock;
+  const int nwin = (nblk + kWindowBlocks - 1) / kWindowBlocks;
+  const int wstride = o.K / 2;
+  const int64_t xstride = Mx<kFmt>::bytes(o.K);
+  // The scale of this lane's block at step st, in byte 0: byte g of the dword
+  // 2 st + s of its row, which the lane of slice st / 2, group 2 (st % 2) + s holds.
+  auto step_scale = [&](uint32_t dwords, int st) {
+    const int from = r8 + 8 * (st >> 1) + 16 * (2 * (st & 1) + slice);
+    return static_cast<uint32_t>(__shfl(static_cast<int>(dwords), from)) >> (8 * g);
+  };
+  const int64_t wrow0 = static_cast<int64_t>(e) * o.N + n0;
+  const __amdgpu_buffer_rsrc_t wres = resource(o.wq + wrow0 * wstride, int64_t{kFewRows} * wstride);
+  const uint8_t* const wsp = o.ws + (wrow0 + r8) * nblk;
+
+  for (int tok0 = 0; tok0 < rows; tok0 += pass) {
+    const int ntok = min(rows - tok0, pass);
+    float* const mypart = part + wave * pass * kFewRows;
+    // Expert row of this lane's token in the group from t0 (rows past the last
+    // repeat it; never stored), and its pair, which is asked for ahead of the
+    // weights: loads return in order.
+    auto row_of = [&](int t0) { return seg0 + tok0 + min(t0 + r8, ntok - 1); };
+    int pair = kGather ? gidx[row_of(0)] : 0;
+    for (int win = wave; win < nwin; win += kFewWaves) {
+      const int sblk = win * kWindowBlocks + slice * 16 + g * 4;  // the blocks whose scales this lane loads
+      const int blk = win * kWindowBlocks + slice * 4 + g;       // this lane's block at step 0 (+ 8 a step)
+      u32x4_t w[4][4];
+      uint32_t sw[4];
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg)
+        sw[rg] = scales4<kDwords>(wsp + static_cast<int64_t>(rg) * 8 * nblk, sblk, nblk);
+      // (No branch for whole windows: past one the compiler no longer counts
+      // the loads in flight and waits for all of them.)
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg)
+#pragma unroll
+        for (int st = 0; st < 4; ++st)  // blocks past K load as zero codes (aux 2: non-temporal)
+          w[rg][st] = __builtin_amdgcn_raw_buffer_load_b128(
+              wres, blk + st * 8 < nblk ? r8 * wstride + (blk + st * 8) * 16 : kOutside, rg * 8 * wstride, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      for (int t0 = 0; t0 < ntok; t0 += 8) {
+        int64_t src = row_of(t0);
+        if constexpr (kGather) {
+          const unsigned u = static_cast<unsigned>(pair) / static_cast<unsigned>(gdiv);
+          src = u < static_cast<unsigned>(src_rows) ? u : 0u;
+          if (ntok > 8) pair = gidx[row_of(t0 + 8 < ntok ? t0 + 8 : 0)];  // of the next group, or the next window's first
+        }
+        u32x4_t x0[4], x1[4];
+        const uint32_t sx = scales4<kDwords>(o.xs + src * nblk, sblk, nblk);
+        const uint8_t* const xp = o.xq + src * xstride;
+        // bytes of a block, and of this lane's (first) chunk in its step-0 block
+        constexpr int kBlockBytes = static_cast<int>(Mx<kFmt>::bytes(kMxBlock));
+        const int xblk = kFmt == kMxFp4 ? blk : win * kWindowBlocks + slice * 4 + (g >> 1);
+        const uint8_t* const xl = xp + (kFmt == kMxFp4 ? 0 : (g & 1) * 16);
+        // a block past K is replaced by the row's first: the weights there are zero
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          const int b0 = xblk + st * 8, b1 = b0 + 2;
+          x0[st] = ld16(xl + (b0 < nblk ? b0 : 0) * kBlockBytes);
+          if constexpr (kFmt == kMxFp8) x1[st] = ld16(xl + (b1 < nblk ? b1 : 0) * kBlockBytes);
+          else x1[st] = u32x4_t{0u, 0u, 0u, 0u};
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4_t acc[4];
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) {
+          acc[rg] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int st = 0; st < 4; ++st)
+            acc[rg] = mx_mfma16<kFmt>(w[rg][st], x0[st], x1[st], acc[rg], step_scale(sw[rg], st), step_scale(sx, st));
+        }
+        // acc[rg][q]: slice lane / 32 of weight row rg*8 + (lane/16 % 2)*4 + q,
+        // token t0 + lane % 8 at its slice lane/8 % 2: matching slices are added.
+        float* const p = mypart + (t0 + r8) * kFewRows + ((lane >> 4) & 1) * 4;
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) {
+          f32x4_t v = acc[rg];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] += __shfl_xor(v[q], 40);
+          if ((lane & 40) == 0) {
+            f32x4_t* const at = reinterpret_cast<f32x4_t*>(p + rg * 8);
+            if (win >= kFewWaves) v += *at;  // not this wave's first window
+            *at = v;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    // thread -> weight row tid % 32 of token tid / 32 (+ 8 per turn)
+    const int wr = tid % kFewRows;
+    const int nw = min(nwin, kFewWaves);
+    for (int tok = tid / kFewRows; (tok & ~7) < ntok; tok += kFewWaves * kWave / kFewRows) {
+      float v = 0.f;
+      for (int w = 0; w < nw; ++w) v += part[(w * pass + tok) * kFewRows + wr];
+      const int r = seg0 + tok0 + tok;
+      if constexpr (kGather) {
+        // an entry that names no token gives a zero row
+        const unsigned u = tok < ntok ? static_cast<unsigned>(gidx[r]) / static_cast<unsigned>(gdiv) : 0u;
+        if (u >= static_cast<unsigned>(src_rows)) v = 0.f;
+      }
+      out.store_one(r, o.N, n0, wr, tok < ntok, v);
+    }
+    __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -680,8 +891,27 @@ hipError_t launch_big(const MxOperands& o, const int32_t* gidx, int gdiv, int sr
 }
 
 template <int kFmt, bool kGather, typename Out>
+hipError_t launch_few(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
+                      hipStream_t stream) {
+  // at most min(E, max_rows) experts have rows
+  const int64_t blocks = static_cast<int64_t>(o.max_rows < o.E ? o.max_rows : o.E) * (o.N / kFewRows);
+  if (blocks > 0x7fffffff || int64_t{kFewRows} * o.K / 2 >= (int64_t{1} << 31)) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kFewWaves * kWave);
+  const int pass = o.rows_bound >= kFewMaxTokens ? kFewMaxTokens : (o.rows_bound + 7) & ~7;
+  const size_t lds = sizeof(float) * kFewWaves * kFewRows * pass;  // at most 32 KB
+  if (o.K % 128 == 0)
+    hipLaunchKernelGGL((mx_product_few<kFmt, kGather, true, Out>), grid, block, lds, stream, o, gidx, gdiv, src_rows,
+                       pass, out);
+  else
+    hipLaunchKernelGGL((mx_product_few<kFmt, kGather, false, Out>), grid, block, lds, stream, o, gidx, gdiv, src_rows,
+                       pass, out);
+  return hipGetLastError();
+}
+
+template <int kFmt, bool kGather, typename Out>
 hipError_t launch_product(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
                           hipStream_t stream) {
+  if (o.rows_bound <= 64) return launch_few<kFmt, kGather>(o, gidx, gdiv, src_rows, out, stream);
   if (o.rows_bound > 64 && big_runs<kFmt>(o, kGather, src_rows))
     return launch_big<kFmt, kGather>(o, gidx, gdiv, src_rows, out, stream);
   const int64_t tiles = (static_cast<int64_t>((o.max_rows + 31) / 32) + o.E) * (o.N / 32);
