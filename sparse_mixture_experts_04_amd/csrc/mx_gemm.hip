@@ -157,103 +157,28 @@ template <typename T> struct DownOut {
   };
 };
 
-// One wave per 32 weight rows x 32 token rows, fragments straight from
-// memory.  The weight rows of the tile are taken in the order pi(x) =
-// 16*((x>>2)&1) + 4*(x>>3) + (x&3), which gives a lane 16 consecutive output
-// columns of its token row.
-template <int kFmt, bool kGather, typename Out>
-__global__ __launch_bounds__(kWave) void mx_product_direct(MxOperands o, const int32_t* __restrict__ gidx, int gdiv,
-                                                           int src_rows, Out out) {
-  const int lane = threadIdx.x;
-  int t_seg0 = 0, t_seg1 = 0;
-  if (lane < o.E) {
-    // offsets come from device memory: clamped, every access stays inside the buffers
-    t_seg0 = min(max(o.offsets[lane], 0), o.max_rows);
-    t_seg1 = min(max(o.offsets[lane + 1], t_seg0), o.max_rows);
-  }
-  const int t_mt = (t_seg1 - t_seg0 + 31) / 32;
-  int t_incl = t_mt;
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const int u = __shfl_up(t_incl, m);
-    if (lane >= m) t_incl += u;
-  }
-  const int ntn = o.N / 32;
-  const int64_t tile = blockIdx.x;
-  const int e = static_cast<int>(__popcll(__ballot(lane < o.E && static_cast<int64_t>(t_incl) * ntn <= tile)));
-  if (e >= o.E) return;
-  const int mt_e = __shfl(t_mt, e);
-  const int64_t local = tile - static_cast<int64_t>(__shfl(t_incl, e) - mt_e) * ntn;
-  const int n0 = static_cast<int>(local / mt_e) * 32;
-  const int m0 = __shfl(t_seg0, e) + static_cast<int>(local % mt_e) * 32;
-  const int rows = min(32, __shfl(t_seg1, e) - m0);
-
-  const int frow = lane & 31;
-  const int half = lane >> 5;
-  const int wrow = ((frow >> 2) & 1) * 16 + (frow >> 3) * 4 + (frow & 3);
-  const int64_t row = m0 + min(frow, rows - 1);
-  int64_t src = row;
-  bool live = true;
-  if constexpr (kGather) {
-    const unsigned u = static_cast<unsigned>(gidx[row]) / static_cast<unsigned>(gdiv);
-    live = u < static_cast<unsigned>(src_rows);
-    src = live ? u : 0;
-  }
-  const int64_t xrow_bytes = Mx<kFmt>::bytes(o.K);
-  const uint8_t* xp = o.xq + src * xrow_bytes + half * 16;
-  const uint8_t* xsp = o.xs + src * (o.K / kMxBlock) + half;
-  const int64_t wr = static_cast<int64_t>(e) * o.N + n0 + wrow;
-  const uint8_t* wp = o.wq + wr * (o.K / 2) + half * 16;
-  const uint8_t* wsp = o.ws + wr * (o.K / kMxBlock) + half;
-  const u32x4_t zero = {0u, 0u, 0u, 0u};
-
-  f32x16_t acc;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) acc[q] = 0.f;
-  const int steps = o.K / 64;
-  for (int s = 0; s < steps; ++s) {
-    const u32x4_t w = ld16(wp + s * 32);
-    u32x4_t x0, x1 = zero;
-    if constexpr (kFmt == kMxFp4) {
-      x0 = ld16(xp + s * 32);
-    } else {
-      x0 = ld16(xp + s * 64);
-      x1 = ld16(xp + s * 64 + 32);
-    }
-    const int sw = wsp[s * 2];
-    const int sx = live ? xsp[s * 2] : 0;
-    acc = mx_mfma32<kFmt, 0>(frag(w, zero), frag(live ? x0 : zero, live ? x1 : zero), acc, sw, sx);
-  }
-  float v[16];
-#pragma unroll
-  for (int q = 0; q < 16; ++q) v[q] = acc[q];
-  const typename Out::Tile to(out, m0, rows, o.N);
-  to.store_scale(frow, n0, half, to.store(frow, n0, half, v));
-}
-
 // ---------------------------------------------------------------------------
-// Few rows per expert (decode): the product is bound by streaming each active
-// expert's weights once.  A block of four waves owns 32 weight rows (one MX
-// block of the result), its waves windows of 1024 of K in turn; every wave
-// asks for its whole window, 16 KB, before the first MFMA, so that with about
-// 16 waves on a CU 256 KB of it are on their way.
+// Few rows per expert: bound by streaming each active expert's weights.  A
+// block of four waves owns 32 weight rows (one MX block of the result) and a
+// chunk of up to `chunk` of the expert's token rows; its waves take windows of K
+// (1024, or 512 where K is short) in turn, and every wave asks for its whole
+// window, 16 KB, before the first MFMA: with about 12 waves on a CU 192 KB of
+// weights are on their way.  The chunks of one expert's weight rows are
+// neighbours on one XCD, so its L2 serves the weights to all but the first.
 //
 // One 16x16x128 scaled MFMA takes 8 weight rows x 2 K-slices (operand A) and 8
 // token rows x the same 2 slices (operand B); of its 16x16 results those of
-// matching slices are wanted, and a lane exchange adds the two.  So a weight
+// matching slices are wanted, and are added at the end.  So a weight
 // load reads a whole 128-byte line of each of 8 rows: lane (row, slice s, group
 // g) holds, at step t, block 8 t + 4 s + g of its window.  (For e4m3 rows an
 // MFMA's K block b lies in lanes of groups 2 (b % 2) and + 1, halves b / 2;
-// their addresses follow that.)  The scales of a row's window are 8 dwords, one
-// loaded by each of its 8 lanes, and handed round by lane exchanges.
+// their addresses follow that.)  The scales of a row's window are 8 (or 4)
+// dwords, loaded by its lanes, and handed round by lane exchanges.
 // The token groups of 8 are taken in turn under the window's weights, and
-// every wave keeps its partial sums in its own part of LDS; at the end they are
-// added in wave order.  A pass covers up to 64 token rows; an expert with more
-// gets further passes.
+// every wave keeps its partial sums, by slice, in its own part of LDS; at the
+// end they are added in order.
 constexpr int kFewWaves = 4;
 constexpr int kFewRows = 32;
-constexpr int kFewMaxTokens = 64;  // token rows of a pass
-constexpr int kWindowBlocks = 32;  // 1024 of K
 
 // The scales of blocks blk .. blk + 3 of a row of nblk (blk a multiple of 4).
 // kDwords: nblk is a multiple of 4, so rows are whole dwords; else nblk is
@@ -272,17 +197,19 @@ __device__ __forceinline__ uint32_t scales4(const uint8_t* row, int blk, int nbl
   }
 }
 
-template <int kFmt>
+template <int kFmt, int kSel>
 __device__ __forceinline__ f32x4_t mx_mfma16(u32x4_t w, u32x4_t x0, u32x4_t x1, f32x4_t c, uint32_t sw, uint32_t sx) {
   const u32x4_t zero = {0u, 0u, 0u, 0u};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w, zero), frag(x0, x1), c, 4, mx_code<kFmt>(), 0,
-                                                          static_cast<int>(sw), 0, static_cast<int>(sx));
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w, zero), frag(x0, x1), c, 4, mx_code<kFmt>(), kSel,
+                                                          static_cast<int>(sw), kSel, static_cast<int>(sx));
 }
 
-template <int kFmt, bool kGather, bool kDwords, typename Out>
+// kSt: MFMA steps of a window of 256 kSt of K.
+template <int kFmt, bool kGather, bool kDwords, int kSt, typename Out>
 __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o, const int32_t* __restrict__ gidx,
-                                                                   int gdiv, int src_rows, int pass, Out out) {
-  // partial sums: [wave][token of the pass][weight row]
+                                                                   int gdiv, int src_rows, int chunk, Out out) {
+  constexpr int kWindowBlocks = 8 * kSt;
+  // partial sums: [wave][slice][token of the chunk][weight row]
   extern __shared__ __attribute__((aligned(16))) float part[];
   const int tid = threadIdx.x;
   const int lane = tid % kWave;
@@ -293,19 +220,17 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
     t_seg0 = min(max(o.offsets[lane], 0), o.max_rows);
     t_seg1 = min(max(o.offsets[lane + 1], t_seg0), o.max_rows);
   }
-  // the block's expert: the (blockIdx.x / n-tiles)-th that has rows
+  // tiles: by expert, 32 weight rows, chunk (fastest); a run of them for each XCD
+  const int t_chunks = (t_seg1 - t_seg0 + chunk - 1) / chunk;
   const int ntn = o.N / kFewRows;
-  const int nth = blockIdx.x / ntn;
-  const bool active = t_seg1 > t_seg0;
-  const unsigned long long mask = __ballot(active);
-  const unsigned long long mine =
-      __ballot(active && __popcll(mask & ((1ull << lane) - 1)) == nth);
-  if (mine == 0) return;
-  const int e = __builtin_amdgcn_readfirstlane(__ffsll(mine) - 1);
-  const int n0 = (blockIdx.x - nth * ntn) * kFewRows;
-  const int seg0 = __builtin_amdgcn_readlane(t_seg0, e);
-  const int rows = __builtin_amdgcn_readlane(t_seg1, e) - seg0;
-
+  int t_incl = t_chunks;
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) {
+    const int u = __shfl_up(t_incl, m);
+    if (lane >= m) t_incl += u;
+  }
+  const int total = __builtin_amdgcn_readlane(t_incl, o.E - 1) * ntn;
+  const int per_xcd = (total + 7) / 8;
   const int r8 = lane & 7;
   const int slice = (lane >> 3) & 1;
   const int g = lane >> 4;
@@ -313,28 +238,45 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
   const int nwin = (nblk + kWindowBlocks - 1) / kWindowBlocks;
   const int wstride = o.K / 2;
   const int64_t xstride = Mx<kFmt>::bytes(o.K);
-  // The scale of this lane's block at step st, in byte 0: byte g of the dword
-  // 2 st + s of its row, which the lane of slice st / 2, group 2 (st % 2) + s holds.
-  auto step_scale = [&](uint32_t dwords, int st) {
-    const int from = r8 + 8 * (st >> 1) + 16 * (2 * (st & 1) + slice);
-    return static_cast<uint32_t>(__shfl(static_cast<int>(dwords), from)) >> (8 * g);
+  // The scales of this lane's blocks, step st's in byte st: byte g of the dword 2 st + s of its row.  Dword j is in
+  // the lane of slice j / 4, group j % 4.
+  auto step_scales = [&](uint32_t dwords) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int st = 0; st < kSt; ++st) {
+      const int from = r8 + 8 * (st >> 1) + 16 * (2 * (st & 1) + slice);
+      v |= (static_cast<uint32_t>(__shfl(static_cast<int>(dwords), from)) >> (8 * g) & 255u) << (8 * st);
+    }
+    return v;
   };
-  const int64_t wrow0 = static_cast<int64_t>(e) * o.N + n0;
-  const __amdgpu_buffer_rsrc_t wres = resource(o.wq + wrow0 * wstride, int64_t{kFewRows} * wstride);
-  const uint8_t* const wsp = o.ws + (wrow0 + r8) * nblk;
+  // (the grid covers the tiles that the rows' bound allows; offsets beyond it take further turns)
+  for (int at = blockIdx.x >> 3; at < per_xcd; at += gridDim.x >> 3) {
+    const int tile = (blockIdx.x & 7) * per_xcd + at;
+    if (tile >= total) break;
+    const int e = __builtin_amdgcn_readfirstlane(
+        static_cast<int>(__popcll(__ballot(lane < o.E && t_incl * ntn <= tile))));
+    const int chunks_e = __builtin_amdgcn_readlane(t_chunks, e);
+    const int local = tile - (__builtin_amdgcn_readlane(t_incl, e) - chunks_e) * ntn;
+    const int n0 = __builtin_amdgcn_readfirstlane(local / chunks_e * kFewRows);
+    const int seg1 = __builtin_amdgcn_readlane(t_seg1, e);
+    const int row0 = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_readlane(t_seg0, e) + local % chunks_e * chunk);
+    const int ntok = min(seg1 - row0, chunk);
 
-  for (int tok0 = 0; tok0 < rows; tok0 += pass) {
-    const int ntok = min(rows - tok0, pass);
-    float* const mypart = part + wave * pass * kFewRows;
+    const int64_t wrow0 = static_cast<int64_t>(e) * o.N + n0;
+    const __amdgpu_buffer_rsrc_t wres = resource(o.wq + wrow0 * wstride, int64_t{kFewRows} * wstride);
+    const uint8_t* const wsp = o.ws + (wrow0 + r8) * nblk;
+
+    float* const mypart = part + (wave * 2 + slice) * chunk * kFewRows;
     // Expert row of this lane's token in the group from t0 (rows past the last
     // repeat it; never stored), and its pair, which is asked for ahead of the
     // weights: loads return in order.
-    auto row_of = [&](int t0) { return seg0 + tok0 + min(t0 + r8, ntok - 1); };
+    auto row_of = [&](int t0) { return row0 + min(t0 + r8, ntok - 1); };
     int pair = kGather ? gidx[row_of(0)] : 0;
     for (int win = wave; win < nwin; win += kFewWaves) {
-      const int sblk = win * kWindowBlocks + slice * 16 + g * 4;  // the blocks whose scales this lane loads
+      // the blocks whose scales this lane loads (the window's 2 kSt dwords; with fewer than 8 the rest repeat them)
+      const int sblk = win * kWindowBlocks + (slice * 16 + g * 4) % kWindowBlocks;
       const int blk = win * kWindowBlocks + slice * 4 + g;       // this lane's block at step 0 (+ 8 a step)
-      u32x4_t w[4][4];
+      u32x4_t w[4][kSt];
       uint32_t sw[4];
 #pragma unroll
       for (int rg = 0; rg < 4; ++rg)
@@ -344,10 +286,12 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
 #pragma unroll
       for (int rg = 0; rg < 4; ++rg)
 #pragma unroll
-        for (int st = 0; st < 4; ++st)  // blocks past K load as zero codes (aux 2: non-temporal)
+        for (int st = 0; st < kSt; ++st)  // blocks past K load as zero codes (aux 2: non-temporal)
           w[rg][st] = __builtin_amdgcn_raw_buffer_load_b128(
               wres, blk + st * 8 < nblk ? r8 * wstride + (blk + st * 8) * 16 : kOutside, rg * 8 * wstride, 2);
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int rg = 0; rg < 4; ++rg) sw[rg] = step_scales(sw[rg]);
       for (int t0 = 0; t0 < ntok; t0 += 8) {
         int64_t src = row_of(t0);
         if constexpr (kGather) {
@@ -355,7 +299,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
           src = u < static_cast<unsigned>(src_rows) ? u : 0u;
           if (ntok > 8) pair = gidx[row_of(t0 + 8 < ntok ? t0 + 8 : 0)];  // of the next group, or the next window's first
         }
-        u32x4_t x0[4], x1[4];
+        u32x4_t x0[kSt], x1[kSt];
         const uint32_t sx = scales4<kDwords>(o.xs + src * nblk, sblk, nblk);
         const uint8_t* const xp = o.xq + src * xstride;
         // bytes of a block, and of this lane's (first) chunk in its step-0 block
@@ -364,33 +308,38 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
         const uint8_t* const xl = xp + (kFmt == kMxFp4 ? 0 : (g & 1) * 16);
         // a block past K is replaced by the row's first: the weights there are zero
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
+        for (int st = 0; st < kSt; ++st) {
           const int b0 = xblk + st * 8, b1 = b0 + 2;
           x0[st] = ld16(xl + (b0 < nblk ? b0 : 0) * kBlockBytes);
           if constexpr (kFmt == kMxFp8) x1[st] = ld16(xl + (b1 < nblk ? b1 : 0) * kBlockBytes);
           else x1[st] = u32x4_t{0u, 0u, 0u, 0u};
         }
         __builtin_amdgcn_sched_barrier(0);
+        const uint32_t sxs = step_scales(sx);
         f32x4_t acc[4];
 #pragma unroll
         for (int rg = 0; rg < 4; ++rg) {
           acc[rg] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int st = 0; st < 4; ++st)
-            acc[rg] = mx_mfma16<kFmt>(w[rg][st], x0[st], x1[st], acc[rg], step_scale(sw[rg], st), step_scale(sx, st));
+          acc[rg] = mx_mfma16<kFmt, 0>(w[rg][0], x0[0], x1[0], acc[rg], sw[rg], sxs);
+          acc[rg] = mx_mfma16<kFmt, 1>(w[rg][1], x0[1], x1[1], acc[rg], sw[rg], sxs);
+          if constexpr (kSt == 4) {
+            acc[rg] = mx_mfma16<kFmt, 2>(w[rg][2], x0[2], x1[2], acc[rg], sw[rg], sxs);
+            acc[rg] = mx_mfma16<kFmt, 3>(w[rg][3], x0[3], x1[3], acc[rg], sw[rg], sxs);
+          }
         }
+        // Pin the MFMAs here, where all lanes are active: the compiler would
+        // move them, and with them their operands' last steps, under the branch.
+#pragma unroll
+        for (int rg = 0; rg < 4; ++rg) asm volatile("" : "+v"(acc[rg]));
         // acc[rg][q]: slice lane / 32 of weight row rg*8 + (lane/16 % 2)*4 + q,
-        // token t0 + lane % 8 at its slice lane/8 % 2: matching slices are added.
-        float* const p = mypart + (t0 + r8) * kFewRows + ((lane >> 4) & 1) * 4;
+        // token t0 + lane % 8 at its slice lane/8 % 2: kept where they match.
+        if ((lane >> 5) == slice) {
+          float* const p = mypart + (t0 + r8) * kFewRows + (g & 1) * 4;
 #pragma unroll
-        for (int rg = 0; rg < 4; ++rg) {
-          f32x4_t v = acc[rg];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += __shfl_xor(v[q], 40);
-          if ((lane & 40) == 0) {
+          for (int rg = 0; rg < 4; ++rg) {
             f32x4_t* const at = reinterpret_cast<f32x4_t*>(p + rg * 8);
-            if (win >= kFewWaves) v += *at;  // not this wave's first window
-            *at = v;
+            if (win >= kFewWaves) acc[rg] += *at;  // not this wave's first window
+            *at = acc[rg];
           }
         }
       }
@@ -398,11 +347,11 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
     __syncthreads();
     // thread -> weight row tid % 32 of token tid / 32 (+ 8 per turn)
     const int wr = tid % kFewRows;
-    const int nw = min(nwin, kFewWaves);
+    const int nw = min(nwin, kFewWaves) * 2;
     for (int tok = tid / kFewRows; (tok & ~7) < ntok; tok += kFewWaves * kWave / kFewRows) {
       float v = 0.f;
-      for (int w = 0; w < nw; ++w) v += part[(w * pass + tok) * kFewRows + wr];
-      const int r = seg0 + tok0 + tok;
+      for (int w = 0; w < nw; ++w) v += part[(w * chunk + tok) * kFewRows + wr];
+      const int r = row0 + tok;
       if constexpr (kGather) {
         // an entry that names no token gives a zero row
         const unsigned u = tok < ntok ? static_cast<unsigned>(gidx[r]) / static_cast<unsigned>(gdiv) : 0u;
@@ -415,15 +364,20 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
 }
 
 // ---------------------------------------------------------------------------
-// Main kernel: 256x256 tiles, 8 waves of 128 token rows x 64 weight rows on
-// 32x32x64 scaled MFMAs, fed by direct buffer->LDS loads.
+// Tiled kernel on 32x32x64 scaled MFMAs, fed by direct buffer->LDS loads, in
+// two shapes:
+//   Big: 256 token rows x 256 weight rows, 8 waves of 128 x 64: the least
+//     traffic per product.
+//   Mid: 64 token rows x 128 weight rows, 4 waves of 64 x 32, with deep rings,
+//     for experts of some dozen rows: bound by the weight stream and its
+//     latency, so more tiles and more stages in flight.
 //
 // * A stage is 128 bytes of every token row (256 of K in e2m1, 128 in e4m3)
-//   and the same K of 256 weight rows.  LDS (160 KB) holds two token units of
-//   32 KB, 64 KB of weight units (two or four stages) and two chunks of
-//   scales: those of up to 1024 of K of all 512 rows.  The scales come in runs
-//   of 32 bytes per row, not per stage: a stage needs 4 or 8 bytes of a row,
-//   and fetching those alone would move a cache line for each.
+//   and the same K of the weight rows.  LDS holds a ring of token units, a ring
+//   of weight units and two chunks of scales: those of up to 1024 (Mid: 2048)
+//   of K of all the tile's rows.  The scales come in runs of 32 bytes per row,
+//   not per stage: a stage needs 4 or 8 bytes of a row, and fetching those
+//   alone would move a cache line for each.
 // * The streams of weight units, token units and scale chunks run on across
 //   the persistent block's tiles, at most one tile ahead.
 // * Loads go through buffer resources whose range covers only the tile's
@@ -439,27 +393,58 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
 // * Where K ends inside a stage, the token chunks past it are loaded as zero
 //   and the scales past it are masked, so what the weight unit holds there
 //   (e2m1 codes are all finite) adds nothing.
-// Measured on MI355X: 1.72 PFLOP/s with e4m3 rows (8192 tokens, d = 2048, F =
-// 5632, 32 experts, k = 2: both products 0.44 ms, against 3.29 ms for the
-// direct kernel) and 2.83 PFLOP/s with e2m1 rows (16384 tokens, d = 4096, F =
-// 14336, 64 experts, k = 2: 2.72 ms against 34.7).
-constexpr int kBig = 256;
-constexpr int kBigWaves = 8;
-constexpr int kXRow = 128;                       // bytes of a token row per stage
-constexpr int kXUnit = kBig * kXRow;
-constexpr int kWRing = 64 << 10;                 // bytes of the weight ring
-constexpr int kScaleRow = 32;                    // scale bytes of a row per chunk, at most
-constexpr int kScaleUnit = kBig * kScaleRow;     // one operand's chunk
-constexpr int kScaleAt = kWRing + 2 * kXUnit;
-constexpr size_t kBigLds = kScaleAt + 4 * kScaleUnit;  // 160 KB
-static_assert(kBigLds == 160 * 1024, "LDS plan");
-template <int kFmt> struct Big {
-  static constexpr int kStageK = kFmt == kMxFp4 ? 256 : 128;
-  static constexpr int kSteps = kStageK / 64;              // k-steps of one MFMA depth
-  static constexpr int kWRow = kStageK / 2;                // bytes of a weight row per stage
-  static constexpr int kWUnit = kBig * kWRow;
-  static constexpr int kWS = kWRing / kWUnit;              // weight stages in the ring
-  static constexpr int kChunkStages = kScaleRow * kMxBlock / kStageK;
+// Measured on MI355X, Big: 1.72 PFLOP/s with e4m3 rows (8192 tokens, d = 2048,
+// F = 5632, 32 experts, k = 2: both products 0.44 ms) and 2.83 PFLOP/s with e2m1 rows (16384 tokens, d = 4096, F =
+// 14336, 64 experts, k = 2: 2.72 ms).
+constexpr int kXRow = 128;  // bytes of a token row per stage
+constexpr int kRun = 32;    // bytes of a row's scales that one load covers
+template <int kFmt> struct Stage {
+  static constexpr int kK = kFmt == kMxFp4 ? 256 : 128;
+  static constexpr int kSteps = kK / 64;             // k-steps of one MFMA depth
+  static constexpr int kWRow = kK / 2;               // bytes of a weight row
+  static constexpr int kScales = kK / kMxBlock;      // scale bytes of a row
+};
+// kBM x kBN tile of kWM x kWN waves; kXS, kWS: stages in the token and weight
+// rings (kXS <= kWS); kRuns: runs of scales in a chunk.
+template <int kFmt_> struct BigShape {
+  static constexpr int kFmt = kFmt_, kBM = 256, kBN = 256, kWM = 2, kWN = 4, kXS = 2, kWS = kFmt_ == kMxFp4 ? 2 : 4,
+                       kRuns = 1;
+};
+template <int kFmt_> struct MidShape {
+  static constexpr int kFmt = kFmt_, kBM = 64, kBN = kFmt_ == kMxFp4 ? 64 : 128, kWM = kFmt_ == kMxFp4 ? 2 : 1,
+                       kWN = 4 / kWM, kXS = 4, kWS = kXS, kRuns = kFmt_ == kMxFp4 ? 2 : 1;
+};
+// kOdd: K is an odd multiple of 64, so every second row of scales starts in the
+// middle of a dword.
+template <typename S, bool kOdd> struct Plan {
+  using St = Stage<S::kFmt>;
+  static constexpr int kWaves = S::kWM * S::kWN;
+  static constexpr int kWUnit = S::kBN * St::kWRow;
+  static constexpr int kXUnit = S::kBM * kXRow;
+  static constexpr int kXAt = S::kWS * kWUnit;                 // LDS: weight ring, token ring, scale chunks
+  static constexpr int kScaleAt = kXAt + S::kXS * kXUnit;
+  static constexpr int kChunkW = S::kRuns * S::kBN * kRun;     // a chunk: the weights' runs, then the tokens'
+  static constexpr int kChunk = kChunkW + S::kRuns * S::kBM * kRun;
+  static constexpr size_t kLds = kScaleAt + 2 * kChunk;
+  static constexpr int kPerCu = 160 * 1024 / kLds;             // blocks that fit a CU
+  // (an odd row's scales lie 2 bytes into the first dword)
+  static constexpr int kChunkStages = (S::kRuns * kRun - (kOdd ? 4 : 0)) / St::kScales;
+  static constexpr int kRowsW = S::kBN / kWaves;               // rows of a unit that a wave fills
+  static constexpr int kRowsX = S::kBM / kWaves;
+  static constexpr int kLdW = kRowsW * St::kWRow / 1024;       // 16-byte loads per lane per unit
+  static constexpr int kLdX = kRowsX * kXRow / 1024;
+  static constexpr int kWF = S::kBN / (S::kWN * 32);           // 32-row fragments of a wave
+  static constexpr int kNJ = S::kBM / (S::kWM * 32);
+  // Loads that may be in flight when a stage begins: those issued after the
+  // ones it needs (each stage issues its token unit, then its weight unit).
+  static constexpr int kInFlightShort = (S::kXS - 2) * (kLdW + kLdX);  // the weight ring no longer than the token ring
+  static constexpr int kInFlight = kInFlightShort + (S::kWS > S::kXS ? kLdW : 0);
+  // A chunk of scales is issued in the first stage of the chunk before, at its
+  // end, and has landed kXS - 2 stages later; it is read at the end of that
+  // chunk's last stage.  More than one chunk split K into chunks of at least
+  // (kChunkStages + 1) / 2 stages.
+  static_assert((kChunkStages + 1) / 2 >= (S::kXS > 3 ? S::kXS - 1 : 2), "scale chunks too short for the rings");
+  static_assert(kLds <= 160 * 1024 && kInFlight < 64, "does not fit");
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
@@ -479,24 +464,21 @@ template <int N> __device__ __forceinline__ void wait_vmcnt_lgkm0() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
-template <int kFmt, bool kGather, typename Out>
-__global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o, const int32_t* __restrict__ gidx,
-                                                                   int gdiv, int src_rows, Out out) {
+template <typename S, bool kGather, bool kOdd, typename Out>
+__global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_tiled(MxOperands o, const int32_t* __restrict__ gidx,
+                                                                     int gdiv, int src_rows, Out out) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  using B = Big<kFmt>;
-  constexpr int kSteps = B::kSteps;
-  constexpr int kWRow = B::kWRow;
-  constexpr int kLdW = B::kWUnit / (kBigWaves * 1024);  // 16-byte loads per lane per unit
-  constexpr int kLdX = kXUnit / (kBigWaves * 1024);
-  constexpr int kLd = kLdX + kLdW;
-  constexpr int kWLanes = kWRow / 16;                   // lanes that fill one weight row
-  constexpr int kStageScales = B::kStageK / kMxBlock;   // scale bytes of a row per stage
+  using P = Plan<S, kOdd>;
+  using St = typename P::St;
+  constexpr int kFmt = S::kFmt, kSteps = St::kSteps, kWRow = St::kWRow, kBM = S::kBM, kBN = S::kBN, kLdW = P::kLdW,
+                kLdX = P::kLdX, kLd = kLdX + kLdW, kWF = P::kWF;
+  constexpr int kWLanes = kWRow / 16;  // lanes that fill one weight row
 
   const int tid = threadIdx.x;
   const int lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave >> 2;  // token half: fragments 2j + wm
-  const int wn = wave & 3;   // weight quarter
+  const int wm = wave / S::kWN;  // token part: fragments j * kWM + wm
+  const int wn = wave % S::kWN;  // weight part
 
   // Expert table in registers: lane e has expert e's row segment (clamped:
   // offsets come from device memory) and the count of m-tiles through it.  An
@@ -507,8 +489,8 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
     t_seg1 = min(max(o.offsets[lane + 1], t_seg0), o.max_rows);
   }
   const int t_rows = t_seg1 - t_seg0;
-  const int t_mt = (t_rows + kBig - 1) / kBig;
-  const int t_h = t_mt > 0 ? ((t_rows + t_mt - 1) / t_mt + 31) & ~31 : kBig;
+  const int t_mt = (t_rows + kBM - 1) / kBM;
+  const int t_h = t_mt > 0 ? ((t_rows + t_mt - 1) / t_mt + 31) & ~31 : kBM;
   int t_incl = t_mt;
 #pragma unroll
   for (int m = 1; m < kWave; m <<= 1) {
@@ -516,16 +498,21 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
     if (lane >= m) t_incl += u;
   }
   const int N = o.N, K = o.K, E = o.E;
-  const int n_tiles_n = (N + kBig - 1) / kBig;
+  const int n_tiles_n = (N + kBN - 1) / kBN;
   const int total = __builtin_amdgcn_readlane(t_incl, E - 1) * n_tiles_n;
   const int G = gridDim.x;
-  // Blocks are dealt round-robin to the 8 XCDs: each XCD gets a contiguous run of tiles.
+  // Blocks are dealt round-robin to the 8 XCDs: each XCD gets a contiguous run
+  // of every G tiles, or an eighth of them all if they are fewer.
   int tile = blockIdx.x;
-  if ((G & 7) == 0) tile = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
+  if ((G & 7) == 0) {
+    const int run = total < G ? (total + 7) >> 3 : G >> 3;
+    if (static_cast<int>(blockIdx.x >> 3) >= run) return;
+    tile = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  }
   if (tile >= total) return;
-  const int kstages = (K + B::kStageK - 1) / B::kStageK;
-  // chunks of scales: as equal as can be, so that none has a single stage
-  const int nchunks = (kstages + B::kChunkStages - 1) / B::kChunkStages;
+  const int kstages = (K + St::kK - 1) / St::kK;
+  // chunks of scales: as equal as can be, so that none is short
+  const int nchunks = (kstages + P::kChunkStages - 1) / P::kChunkStages;
   const int chunk_base = kstages / nchunks, chunk_more = kstages % nchunks;
   const int wstride = K / 2;
   const int xstride = static_cast<int>(Mx<kFmt>::bytes(K));
@@ -550,7 +537,7 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
     const int in = local - group * kGroupM * n_tiles_n;
     const int h = __builtin_amdgcn_readlane(t_h, e);
     const int m0 = __builtin_amdgcn_readlane(t_seg0, e) + (first_m + in % gsize) * h;
-    return TileCoord{e, __builtin_amdgcn_readfirstlane(m0), __builtin_amdgcn_readfirstlane((in / gsize) * kBig),
+    return TileCoord{e, __builtin_amdgcn_readfirstlane(m0), __builtin_amdgcn_readfirstlane((in / gsize) * kBN),
                      __builtin_amdgcn_readfirstlane(min(h, __builtin_amdgcn_readlane(t_seg1, e) - m0))};
   };
   auto key_x = [](int r) { return (r >> 1) & 7; };
@@ -559,32 +546,38 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
     return kWRow == 128 ? ((r >> 1) & 3) | (((r >> 4) & 1) << 2) : ((r >> 2) & 1) | (((r >> 4) & 1) << 1);
   };
 
-  // ---- producers.  This wave fills rows wave*32 .. +31 of every unit: a load
-  // instruction moves 1 KB, 8 token rows (or 8 or 16 weight rows).
-  const int srow = wave * 32 + (lane >> 3);  // token and scale rows: + 8 i
-  int vw[kLdW], vx[4], vs[4], vt[4];  // offsets of weight, token, token-scale and weight-scale loads
-  bool past[4];                       // this lane's token chunk lies past K in the last stage
+  // Offset of a row's scales, down to a whole dword.
+  auto scale_offset = [&](int row) { return row * sstride - (kOdd ? (row & 1) * 2 : 0); };
+
+  // ---- producers.  This wave fills kRowsW and kRowsX rows of every unit: a
+  // load instruction moves 1 KB, 8 token rows (or 8 or 16 weight rows), or runs
+  // of 8 rows' scales.
+  constexpr int kTW = P::kRowsW / 8;  // scale loads of a run, weights
+  const int srow = wave * P::kRowsX + (lane >> 3);  // token rows: + 8 i
+  int vw[kLdW], vx[kLdX], vs[kLdX], vt[kTW];  // offsets of weight, token, token-scale and weight-scale loads
+  bool past[kLdX];                            // this lane's token chunk lies past K in the last stage
   const int last_bytes = xstride - (kstages - 1) * kXRow;
 #pragma unroll
   for (int i = 0; i < kLdW; ++i) {
-    const int r = wave * 32 + i * (64 / kWLanes) + lane / kWLanes;
+    const int r = wave * P::kRowsW + i * (64 / kWLanes) + lane / kWLanes;
     vw[i] = r * wstride + (((lane % kWLanes) ^ key_w(r)) << 4);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kTW; ++i) vt[i] = scale_offset(wave * P::kRowsW + 8 * i + (lane >> 3)) + (lane & 7) * 4;
+#pragma unroll
+  for (int i = 0; i < kLdX; ++i) {
     const int r = srow + 8 * i;
     const int c = (lane & 7) ^ key_x(r);
     vx[i] = r * xstride + (c << 4);
     past[i] = (c << 4) >= last_bytes;
-    vt[i] = r * sstride + (lane & 7) * 4;
-    vs[i] = vt[i];
+    vs[i] = scale_offset(r) + (lane & 7) * 4;
   }
   TileCoord cur = coord(tile), nxt = coord(tile + G);
-  int gn[4] = {0, 0, 0, 0};  // gathered: the pairs of rows srow + 8 i of the next tile
+  int gn[kLdX] = {};  // gathered: the pairs of rows srow + 8 i of the next tile
   auto load_gidx = [&](const TileCoord& t) {
     const __amdgpu_buffer_rsrc_t rsrc = resource(gidx + t.m0, t.rows * 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) gn[i] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, (srow + 8 * i) * 4, 0, 0);
+    for (int i = 0; i < kLdX; ++i) gn[i] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, (srow + 8 * i) * 4, 0, 0);
   };
   // Source row of row srow + 8 i of tile t (whose pairs gn holds), or -1: past the tile, or no token.
   auto source = [&](const TileCoord& t, int i) {
@@ -598,7 +591,7 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
   auto to_w = [&](const TileCoord& t) {
     w_ks = 0;
     w_base = o.wq + (static_cast<int64_t>(t.e) * N + t.n0) * wstride;
-    w_rows = t.rows > 0 ? min(N - t.n0, kBig) : 0;
+    w_rows = t.rows > 0 ? min(N - t.n0, kBN) : 0;
   };
   auto to_x = [&](const TileCoord& t) {
     x_ks = 0;
@@ -606,7 +599,7 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
       x_base = o.xq;
       x_rows = t.rows > 0 ? src_rows : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kLdX; ++i) {
         const int s = source(t, i);
         vx[i] = s < 0 ? kOutside : s * xstride + (((lane & 7) ^ key_x(srow + 8 * i)) << 4);
       }
@@ -618,15 +611,22 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
   auto to_scales = [&](const TileCoord& t) {
     c_chunk = c_start = 0;
     cw_base = o.ws + (static_cast<int64_t>(t.e) * N + t.n0) * sstride;
-    cw_rows = t.rows > 0 ? min(N - t.n0, kBig) : 0;
+    cw_rows = t.rows > 0 ? min(N - t.n0, kBN) : 0;
     if constexpr (kGather) {
       cx_base = o.xs;
       cx_rows = t.rows > 0 ? src_rows : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kLdX; ++i) {
         const int s = source(t, i);
-        vs[i] = s < 0 ? kOutside : s * sstride + (lane & 7) * 4;
+        vs[i] = s < 0 ? kOutside : scale_offset(s) + (lane & 7) * 4;
       }
+    } else if constexpr (kOdd) {
+      // from an even row on, so that its dwords are whole
+      const int lead = t.m0 & 1;
+      cx_base = o.xs + static_cast<int64_t>(t.m0 - lead) * sstride;
+      cx_rows = t.rows > 0 ? t.rows + lead : 0;
+#pragma unroll
+      for (int i = 0; i < kLdX; ++i) vs[i] = scale_offset(srow + 8 * i + lead) + (lane & 7) * 4;
     } else {
       cx_base = o.xs + static_cast<int64_t>(t.m0) * sstride;
       cx_rows = t.rows;
@@ -642,53 +642,58 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
   };
   auto refill = [&]() {
     return Refill{rows_from(x_base, x_rows, xstride, x_ks * kXRow), rows_from(w_base, w_rows, wstride, w_ks * kWRow),
-                  smem + kWRing + x_slot * kXUnit + wave * 32 * kXRow, smem + w_slot * B::kWUnit + wave * 32 * kWRow,
+                  smem + P::kXAt + x_slot * P::kXUnit + wave * P::kRowsX * kXRow,
+                  smem + w_slot * P::kWUnit + wave * P::kRowsW * kWRow,
                   x_ks + 1 == kstages};
   };
-  // Load i of a stage's kLd: the token unit first, so that a wait that leaves
-  // kLdW loads in flight covers it.
+  // Load i of a stage's kLd: the token unit first.
   auto issue = [&](const Refill& f, int i) {
     if (i < kLdX) load_lds<16>(f.xr, f.xd + i * 1024, f.last && past[i] ? kOutside : vx[i]);
     else load_lds<16>(f.wr, f.wd + (i - kLdX) * 1024, vw[i - kLdX]);
   };
   auto advance_w = [&]() {
-    w_slot = w_slot + 1 == B::kWS ? 0 : w_slot + 1;
+    w_slot = w_slot + 1 == S::kWS ? 0 : w_slot + 1;
     ++w_ks;
   };
   auto advance_x = [&]() {
-    x_slot ^= 1;
+    x_slot = x_slot + 1 == S::kXS ? 0 : x_slot + 1;
     ++x_ks;
   };
-  // A row's bytes past its last scale are the next row's, or zero past the
-  // range (dword loads: K is a multiple of 128, so a dword lies in one row).
+  // Dword loads.  A row's bytes past its last scale are the next row's, or zero
+  // past the range, which ends with a whole dword (an odd row's last one holds
+  // 2 bytes of the row after it, or past the array's end: not used).
   auto issue_scales = [&]() {
-    const __amdgpu_buffer_rsrc_t wr = rows_from(cw_base, cw_rows, sstride, c_start * kStageScales);
-    const __amdgpu_buffer_rsrc_t xr = rows_from(cx_base, cx_rows, sstride, c_start * kStageScales);
-    unsigned char* dst = smem + kScaleAt + c_slot * 2 * kScaleUnit + wave * 32 * kScaleRow;
+    const __amdgpu_buffer_rsrc_t wr = resource(cw_base + c_start * St::kScales, max((cw_rows * sstride + 3) / 4 * 4 - c_start * St::kScales, 0));
+    const __amdgpu_buffer_rsrc_t xr = resource(cx_base + c_start * St::kScales, max((cx_rows * sstride + 3) / 4 * 4 - c_start * St::kScales, 0));
+    unsigned char* wd = smem + P::kScaleAt + c_slot * P::kChunk + wave * P::kRowsW * kRun;
+    unsigned char* xd = smem + P::kScaleAt + c_slot * P::kChunk + P::kChunkW + wave * P::kRowsX * kRun;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      load_lds<4>(wr, dst + i * 256, vt[i]);
-      load_lds<4>(xr, dst + kScaleUnit + i * 256, vs[i]);
+    for (int run = 0; run < S::kRuns; ++run) {
+#pragma unroll
+      for (int i = 0; i < kTW; ++i) load_lds<4>(wr, wd + run * kBN * kRun + i * 256, vt[i] + run * kRun);
+#pragma unroll
+      for (int i = 0; i < kLdX; ++i) load_lds<4>(xr, xd + run * kBM * kRun + i * 256, vs[i] + run * kRun);
     }
     c_slot ^= 1;
     c_start += chunk_base + (c_chunk < chunk_more ? 1 : 0);
     ++c_chunk;
   };
 
-  // ---- prologue: the first scale chunk, two token units, kWS weight units
-  // (the host has seen to kstages >= kWS)
+  // ---- prologue: the first scale chunk, kXS token units, kWS weight units
+  // (the host has seen to kstages >= kXS)
   if constexpr (kGather) load_gidx(cur);
   to_w(cur);
   to_x(cur);
   to_scales(cur);
   issue_scales();
 #pragma unroll
-  for (int u = 0; u < B::kWS; ++u) {
+  for (int u = 0; u < S::kWS; ++u) {
+    if (u >= kstages) break;  // a tile shorter than the weight ring: the ring is kept as short
     const Refill f = refill();
 #pragma unroll
     for (int i = 0; i < kLd; ++i)
-      if (u < 2 || i >= kLdX) issue(f, i);
-    if (u < 2) advance_x();
+      if (u < S::kXS || i >= kLdX) issue(f, i);
+    if (u < S::kXS) advance_x();
     advance_w();
   }
 
@@ -700,38 +705,54 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
   int r_w = 0, r_x = 0, r_c = 0, r_cs = 0;  // slots the next fragments are read from; stage within the scale chunk
   int r_chunk = 0;                          // that chunk
   // bytes of the scale words that lie before K, in the last stage of a tile
-  const int tail_steps = kSteps - (kstages * B::kStageK - K) / 64;
+  const int tail_steps = kSteps - (kstages * St::kK - K) / 64;
   const uint32_t tail_mask = kFmt == kMxFp4 ? 0xffffffffu >> (8 * (kSteps - tail_steps))
                                             : (tail_steps == kSteps ? 0x00ff00ffu : 0x000000ffu);
 
-  u32x4_t wf[2][2], xlo[4], xhi[4];  // weight fragments double-buffered; token fragments replaced as they are used
-  uint32_t sw[2], sx[4];             // this stage's scales: byte kk (e2m1) or 2 kk (e4m3) is k-step kk's
+  u32x4_t wf[2][kWF], xlo[P::kNJ], xhi[P::kNJ];  // weight fragments double-buffered; token fragments replaced when used
+  uint32_t sw[kWF], sx[P::kNJ];                  // this stage's scales: byte kk (e2m1) or 2 kk (e4m3) is k-step kk's
   const u32x4_t zero = {0u, 0u, 0u, 0u};
-  const int w_at = (wn * 64 + wrow) * kWRow;
-  const int x_at = kWRing + (wm * 32 + frow) * kXRow;
+  const int w_at = (wn * kWF * 32 + wrow) * kWRow;
+  const int x_at = P::kXAt + (wm * 32 + frow) * kXRow;
   auto read_w = [&](int kk, int i) {
-    return *reinterpret_cast<const u32x4_t*>(smem + r_w * B::kWUnit + i * 32 * kWRow +
+    return *reinterpret_cast<const u32x4_t*>(smem + r_w * P::kWUnit + i * 32 * kWRow +
                                              (w_at + (((kk * 2 + half) ^ kw) << 4)));
   };
   auto read_x = [&](int kk, int j, int hi) {
     const int c = kFmt == kMxFp4 ? kk * 2 + half : kk * 4 + 2 * hi + half;
-    return *reinterpret_cast<const u32x4_t*>(smem + r_x * kXUnit + j * 64 * kXRow + (x_at + ((c ^ kx) << 4)));
+    return *reinterpret_cast<const u32x4_t*>(smem + r_x * P::kXUnit + j * S::kWM * 32 * kXRow + (x_at + ((c ^ kx) << 4)));
   };
-  auto read_scale = [&](int row, uint32_t mask) {
-    const unsigned char* p = smem + kScaleAt + r_c * 2 * kScaleUnit + r_cs * kStageScales + row * kScaleRow;
-    if constexpr (kFmt == kMxFp4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      return __builtin_amdgcn_perm(v.y, v.x, half ? 0x07050301u : 0x06040200u) & mask;
+  // Scales of a row this stage: `at` is its place in the chunk's first run, `rows` those of a run, `odd` whether
+  // its scales start 2 bytes into their dword.
+  auto read_scale = [&](int at, int rows, uint32_t mask, int odd) {
+    const int first_byte = r_cs * St::kScales;
+    auto word = [&](int b) {
+      return reinterpret_cast<const uint32_t*>(smem + P::kScaleAt + r_c * P::kChunk + at + (b / kRun) * rows * kRun +
+                                               b % kRun);
+    };
+    uint32_t lo, hi = 0;
+    if constexpr (kOdd) {
+      const uint32_t w0 = *word(first_byte), w1 = *word(first_byte + 4);
+      lo = __builtin_amdgcn_alignbit(w1, w0, 16 * odd);
+      if constexpr (kFmt == kMxFp4) hi = __builtin_amdgcn_alignbit(*word(first_byte + 8), w1, 16 * odd);
+    } else if constexpr (kFmt == kMxFp4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(word(first_byte));
+      lo = v.x;
+      hi = v.y;
     } else {
-      return (*reinterpret_cast<const uint32_t*>(p) >> (8 * half)) & mask;
+      lo = *word(first_byte);
     }
+    if constexpr (kFmt == kMxFp4) return __builtin_amdgcn_perm(hi, lo, half ? 0x07050301u : 0x06040200u) & mask;
+    else return (lo >> (8 * half)) & mask;
   };
+  int x_odd[P::kNJ] = {};  // kOdd: whether the lane's token rows are odd rows of xs
   auto read_scales = [&](auto nj_c, bool last) {
     const uint32_t mask = last ? tail_mask : 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sw[i] = read_scale(wn * 64 + i * 32 + wrow, mask);
+    for (int i = 0; i < kWF; ++i) sw[i] = read_scale((wn * kWF * 32 + i * 32 + wrow) * kRun, kBN, mask, wrow & 1);
 #pragma unroll
-    for (int j = 0; j < decltype(nj_c)::value; ++j) sx[j] = read_scale(kBig + (2 * j + wm) * 32 + frow, mask);
+    for (int j = 0; j < decltype(nj_c)::value; ++j)
+      sx[j] = read_scale(P::kChunkW + ((j * S::kWM + wm) * 32 + frow) * kRun, kBM, mask, x_odd[j]);
   };
   auto barrier = [&]() {
     asm volatile("" ::: "memory");
@@ -744,26 +765,39 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
 
   auto run_tile = [&](auto nj_c) {
     constexpr int NJ = decltype(nj_c)::value;
-    f32x16_t acc[2][NJ];
+    f32x16_t acc[kWF][NJ];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kWF; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    if constexpr (kOdd) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int r = (j * S::kWM + wm) * 32 + frow;
+        if constexpr (kGather) {
+          const __amdgpu_buffer_rsrc_t rsrc = resource(gidx + cur.m0, cur.rows * 4);  // zero past the tile
+          x_odd[j] = static_cast<unsigned>(__builtin_amdgcn_raw_buffer_load_b32(rsrc, r * 4, 0, 0)) /
+                     static_cast<unsigned>(gdiv) & 1;
+        } else {
+          x_odd[j] = (cur.m0 + r) & 1;
+        }
+      }
+    }
     // k-step 0 of the tile (the previous tile's last block read it with that tile's NJ)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) wf[0][i] = read_w(0, i);
+    for (int i = 0; i < kWF; ++i) wf[0][i] = read_w(0, i);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       xlo[j] = read_x(0, j, 0);
       if constexpr (kFmt == kMxFp8) xhi[j] = read_x(0, j, 1);
     }
-    read_scales(nj_c, kstages == 1);
+    read_scales(nj_c, false);
 
-    // One k-step: its 2 NJ MFMAs, each token fragment replaced by that of
+    // One k-step: its kWF NJ MFMAs, each token fragment replaced by that of
     // `next` once used, and (last) the loads that refill the freed slots.
-    auto block = [&](auto kk_c, auto next_c, auto last_c, u32x4_t (&wa)[2], u32x4_t (&wb)[2]) {
+    auto block = [&](auto kk_c, auto next_c, auto last_c, u32x4_t (&wa)[kWF], u32x4_t (&wb)[kWF]) {
       constexpr int kk = decltype(kk_c)::value, next = decltype(next_c)::value;
       constexpr int kSel = kFmt == kMxFp4 ? kk : 2 * kk;
       Refill f;
@@ -771,7 +805,7 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kWF; ++i) {
           acc[i][j] = mx_mfma32<kFmt, kSel>(frag(wa[i], zero), frag(xlo[j], kFmt == kMxFp8 ? xhi[j] : zero), acc[i][j],
                                             static_cast<int>(sw[i]), static_cast<int>(sx[j]));
           if (j == 0) wb[i] = read_w(next, i);
@@ -787,7 +821,7 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
       // Pin the accumulators here: the compiler would else sink the MFMAs
       // past the stage's branches to its end, with every fragment live.
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < kWF; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
     };
@@ -800,22 +834,21 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
         block(integral_constant<int, 1>{}, integral_constant<int, 2>{}, no, wf[1], wf[0]);
         block(integral_constant<int, 2>{}, integral_constant<int, 3>{}, no, wf[0], wf[1]);
       }
-      // The next stage must have landed; with a longer weight ring the last
-      // weight unit issued is for a later one.  lgkmcnt(0): this wave's reads
-      // of the stage are complete, so after the barrier its units are free.
-      wait_vmcnt_lgkm0<(B::kWS > 2 ? kLdW : 0)>();
+      // The next stage must have landed.  lgkmcnt(0): this wave's reads of the
+      // stage are complete, so after the barrier its units are free.
+      if (S::kWS > S::kXS && kstages < S::kWS) wait_vmcnt_lgkm0<P::kInFlightShort>();
+      else wait_vmcnt_lgkm0<P::kInFlight>();
       barrier();
       __builtin_amdgcn_sched_barrier(0);
-      // The first stage of a scale chunk: the other chunk slot is free, and
-      // the chunk has a second stage whose wait covers these loads.
+      // The first stage of a scale chunk: the other chunk slot is free.
       if (r_cs == 0) {
         if (c_chunk == nchunks) to_scales(nxt);
         issue_scales();
       }
       if (x_ks == kstages) to_x(nxt);
       if (w_ks == kstages) to_w(nxt);
-      r_w = r_w + 1 == B::kWS ? 0 : r_w + 1;
-      r_x ^= 1;
+      r_w = r_w + 1 == S::kWS ? 0 : r_w + 1;
+      r_x = r_x + 1 == S::kXS ? 0 : r_x + 1;
       if (++r_cs == chunk_base + (r_chunk < chunk_more ? 1 : 0)) {
         r_cs = 0;
         r_c ^= 1;
@@ -827,15 +860,15 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
       read_scales(nj_c, ks + 2 == kstages);
     }
 
-    // acc[i][j][q]: tile row (2j + wm)*32 + frow, column wn*64 + i*32 + 16 half + q.
+    // acc[i][j][q]: tile row (j kWM + wm)*32 + frow, column (wn kWF + i)*32 + 16 half + q.
     const typename Out::Tile to(out, cur.m0, cur.rows, N);
-    const int col = cur.n0 + wn * 64;
+    const int col = cur.n0 + wn * kWF * 32;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int row = (2 * j + wm) * 32 + frow;
-      uint32_t b[2];
+      const int row = (j * S::kWM + wm) * 32 + frow;
+      uint32_t b[kWF];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kWF; ++i) {
         // Redefine the group's accumulators here (an empty asm on their
         // registers): otherwise the compiler copies all of them out of the
         // accumulator registers at the loop exit.
@@ -846,17 +879,21 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
         b[i] = to.store(row, col + 32 * i, half, v);
         __builtin_amdgcn_sched_barrier(0);
       }
-      to.store_scales(row, col, half, b[0], b[1]);
+      if constexpr (kWF == 2) to.store_scales(row, col, half, b[0], b[1]);
+      else to.store_scale(row, col, half, b[0]);
     }
   };
 
   for (;;) {
     if constexpr (kGather) load_gidx(nxt);
-    const int nj = (((cur.rows + 31) >> 5) + 1) >> 1;  // 1..4
-    if (nj >= 4) run_tile(std::integral_constant<int, 4>{});
-    else if (nj == 3) run_tile(std::integral_constant<int, 3>{});
-    else if (nj == 2) run_tile(std::integral_constant<int, 2>{});
-    else run_tile(std::integral_constant<int, 1>{});
+    const int nj = (((cur.rows + 31) >> 5) + S::kWM - 1) / S::kWM;  // 1..kNJ
+    if constexpr (P::kNJ == 4) {
+      if (nj >= 4) run_tile(std::integral_constant<int, 4>{});
+      else if (nj == 3) run_tile(std::integral_constant<int, 3>{});
+    }
+    if constexpr (P::kNJ >= 2)
+      if (nj == 2) run_tile(std::integral_constant<int, 2>{});
+    if (nj <= 1) run_tile(std::integral_constant<int, 1>{});
     tile += G;
     if (tile >= total) break;
     cur = nxt;
@@ -865,60 +902,103 @@ __global__ __launch_bounds__(kBigWaves * kWave) void mx_product_256(MxOperands o
   wait_vmcnt_lgkm0<0>();
 }
 
-// The 256x256 kernel takes K in multiples of 128 (scale rows of whole dwords)
-// and at least its weight ring long, and 32-bit buffer offsets: 256 rows of K and of the result, and where rows
-// are gathered all of them, below 2^31 bytes.
-template <int kFmt> bool big_runs(const MxOperands& o, bool gather, int src_rows) {
+// The tiled kernels take K at least the token ring long and 32-bit buffer
+// offsets: a tile's rows of K
+// and of the result, and where rows are gathered all of them, below 2^31 bytes.
+template <typename S> bool tiled_runs(const MxOperands& o, bool gather, int src_rows) {
   constexpr int64_t kLimit = int64_t{1} << 31;
-  return o.K % 128 == 0 && o.K > (Big<kFmt>::kWS - 1) * Big<kFmt>::kStageK && int64_t{kBig} * o.K < kLimit && int64_t{kBig} * 4 * o.N < kLimit &&
-         (!gather || Mx<kFmt>::bytes(o.K) * src_rows < kLimit);
+  return o.K > (S::kXS - 1) * Stage<S::kFmt>::kK && int64_t{256} * o.K < kLimit &&
+         int64_t{256} * 4 * o.N < kLimit && (!gather || Mx<S::kFmt>::bytes(o.K) * src_rows < kLimit);
 }
 
-template <int kFmt, bool kGather, typename Out>
-hipError_t launch_big(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
-                      hipStream_t stream) {
+template <typename S, bool kGather, bool kOdd, typename Out>
+hipError_t launch_tiled(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
+                        hipStream_t stream) {
+  using P = Plan<S, kOdd>;
   static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_product_256<kFmt, kGather, Out>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBigLds));
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_product_tiled<S, kGather, kOdd, Out>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::kLds));
   if (attr != hipSuccess) return attr;
   // at most this many tiles
-  const int64_t tiles = (static_cast<int64_t>((o.max_rows + kBig - 1) / kBig) + o.E) * ((o.N + kBig - 1) / kBig);
+  const int64_t tiles = (static_cast<int64_t>((o.max_rows + S::kBM - 1) / S::kBM) + o.E) * ((o.N + S::kBN - 1) / S::kBN);
   if (tiles > 0x7fffffff) return hipErrorInvalidValue;
-  const int64_t cus = device_cu_count();
-  hipLaunchKernelGGL((mx_product_256<kFmt, kGather, Out>), dim3(static_cast<unsigned>(tiles < cus ? tiles : cus)),
-                     dim3(kBigWaves * kWave), kBigLds, stream, o, gidx, gdiv, src_rows, out);
+  const int64_t most = int64_t{device_cu_count()} * P::kPerCu;
+  hipLaunchKernelGGL((mx_product_tiled<S, kGather, kOdd, Out>), dim3(static_cast<unsigned>(tiles < most ? tiles : most)),
+                     dim3(P::kWaves * kWave), P::kLds, stream, o, gidx, gdiv, src_rows, out);
+  return hipGetLastError();
+}
+
+template <typename S, bool kGather, typename Out>
+hipError_t launch_tiled(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
+                        hipStream_t stream) {
+  return o.K % 128 == 0 ? launch_tiled<S, kGather, false>(o, gidx, gdiv, src_rows, out, stream)
+                        : launch_tiled<S, kGather, true>(o, gidx, gdiv, src_rows, out, stream);
+}
+
+// Token rows of a block: all that an expert can have, up to 32 (16 and 32 measured: 91 and 81 us at 42 rows per expert).
+int few_chunk(const MxOperands& o) { return o.rows_bound <= 8 ? 8 : o.rows_bound <= 16 ? 16 : 32; }
+
+template <int kFmt, bool kGather, bool kDwords, int kSt, typename Out>
+hipError_t launch_few(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
+                      hipStream_t stream) {
+  const int chunk = few_chunk(o);
+  // (expert, chunk) pairs: each expert with rows has at most one chunk that is not full
+  const int64_t active = o.max_rows < o.E ? o.max_rows : o.E;
+  const int64_t rows = int64_t{o.rows_bound} * o.E < o.max_rows ? int64_t{o.rows_bound} * o.E : o.max_rows;
+  const int64_t chunks = o.rows_bound <= chunk ? active : rows / chunk + active;
+  const int64_t blocks = (chunks * (o.N / kFewRows) + 7) / 8 * 8;
+  if (blocks > 0x7fffffff || int64_t{kFewRows} * o.K / 2 >= (int64_t{1} << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((mx_product_few<kFmt, kGather, kDwords, kSt, Out>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(kFewWaves * kWave), sizeof(float) * 2 * kFewWaves * kFewRows * chunk, stream, o, gidx, gdiv,
+                     src_rows, chunk, out);
   return hipGetLastError();
 }
 
 template <int kFmt, bool kGather, typename Out>
 hipError_t launch_few(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
                       hipStream_t stream) {
-  // at most min(E, max_rows) experts have rows
-  const int64_t blocks = static_cast<int64_t>(o.max_rows < o.E ? o.max_rows : o.E) * (o.N / kFewRows);
-  if (blocks > 0x7fffffff || int64_t{kFewRows} * o.K / 2 >= (int64_t{1} << 31)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kFewWaves * kWave);
-  const int pass = o.rows_bound >= kFewMaxTokens ? kFewMaxTokens : (o.rows_bound + 7) & ~7;
-  const size_t lds = sizeof(float) * kFewWaves * kFewRows * pass;  // at most 32 KB
+  // four windows of 512 where they cover K, else of 1024
   if (o.K % 128 == 0)
-    hipLaunchKernelGGL((mx_product_few<kFmt, kGather, true, Out>), grid, block, lds, stream, o, gidx, gdiv, src_rows,
-                       pass, out);
-  else
-    hipLaunchKernelGGL((mx_product_few<kFmt, kGather, false, Out>), grid, block, lds, stream, o, gidx, gdiv, src_rows,
-                       pass, out);
-  return hipGetLastError();
+    return o.K <= 2048 ? launch_few<kFmt, kGather, true, 2>(o, gidx, gdiv, src_rows, out, stream)
+                       : launch_few<kFmt, kGather, true, 4>(o, gidx, gdiv, src_rows, out, stream);
+  return o.K <= 2048 ? launch_few<kFmt, kGather, false, 2>(o, gidx, gdiv, src_rows, out, stream)
+                     : launch_few<kFmt, kGather, false, 4>(o, gidx, gdiv, src_rows, out, stream);
 }
 
+// Which kernel runs.  rows, active: what the batch can bring in all, and the
+// experts that can have any.  Measured on MI355X (both products, us; fp8: d =
+// 2048, F = 1408, 32 experts, k = 4; fp4: d = 3584, F = 2560, 64 experts, k = 2):
+//   rows per expert       4     8    12    25    42    62    88
+//   fp8  few             32    38    46    62    82   107   134
+//        Mid             31    35    36    39    48    52    60
+//        Big             43    45    46    46    51    57    65
+//   rows per expert       1     3     9    19    31    62
+//   fp4  few             38   117   157   209   272   447
+//        Mid             66   177   184   185   207   260
+//        Big             59   178   183   184   189   213
+// and for one expert (d = F = 2048, fp8) of 100, 200, 400, 3000 rows: few 19, 25, 38, 174, Mid 25, 26, 27, 59, Big 42,
+// 65, 65, 69; fp4, 5000 rows: few 239, Mid 80, Big 55.
+//   few: weights dominate, or all its blocks run at once;
+//   Mid: too few tiles for Big to fill the CUs (half of them, for e2m1 rows);
+//   few also takes what the tiled kernels do not: K shorter than their rings, rows past 32-bit offsets.
 template <int kFmt, bool kGather, typename Out>
 hipError_t launch_product(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
                           hipStream_t stream) {
-  if (o.rows_bound <= 64) return launch_few<kFmt, kGather>(o, gidx, gdiv, src_rows, out, stream);
-  if (o.rows_bound > 64 && big_runs<kFmt>(o, kGather, src_rows))
-    return launch_big<kFmt, kGather>(o, gidx, gdiv, src_rows, out, stream);
-  const int64_t tiles = (static_cast<int64_t>((o.max_rows + 31) / 32) + o.E) * (o.N / 32);
-  if (tiles > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((mx_product_direct<kFmt, kGather, Out>), dim3(static_cast<unsigned>(tiles)), dim3(kWave), 0,
-                     stream, o, gidx, gdiv, src_rows, out);
-  return hipGetLastError();
+  const int64_t bound = int64_t{o.rows_bound} * o.E;
+  const int64_t rows = bound < o.max_rows ? bound : o.max_rows;
+  const int64_t active = rows < o.E ? rows : o.E;
+  const int cus = device_cu_count();
+  const bool few = rows <= (kFmt == kMxFp4 ? 12 : 6) * active ||
+                   (rows / few_chunk(o) + active) * (o.N / kFewRows) <= 3 * cus;
+  if (!few) {
+    const int64_t big_m = (rows + BigShape<kFmt>::kBM - 1) / BigShape<kFmt>::kBM;
+    const int64_t big = (big_m > active ? big_m : active) * ((o.N + BigShape<kFmt>::kBN - 1) / BigShape<kFmt>::kBN);
+    if (big <= (kFmt == kMxFp4 ? cus / 2 : cus) && tiled_runs<MidShape<kFmt>>(o, kGather, src_rows))
+      return launch_tiled<MidShape<kFmt>, kGather>(o, gidx, gdiv, src_rows, out, stream);
+    if (tiled_runs<BigShape<kFmt>>(o, kGather, src_rows))
+      return launch_tiled<BigShape<kFmt>, kGather>(o, gidx, gdiv, src_rows, out, stream);
+  }
+  return launch_few<kFmt, kGather>(o, gidx, gdiv, src_rows, out, stream);
 }
 
 }  // namespace

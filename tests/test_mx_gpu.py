@@ -134,7 +134,9 @@ SHAPES = [(1, 64, 64, 1, 1, -1, None), (1, 256, 128, 8, 2, -1, None), (8, 512, 2
           (333, 640, 448, 8, 4, 100, None), (520, 384, 832, 3, 1, -1, 1), (777, 256, 320, 6, 2, 0, None),
           (1100, 320, 256, 2, 2, -1, None), (400, 2688, 1408, 3, 2, -1, None), (700, 1152, 640, 2, 2, 300, None),
           (261, 768, 2304, 2, 2, -1, None), (3, 4672, 192, 2, 1, -1, None), (20, 128, 4736, 2, 2, -1, None),
-          (50, 8256, 64, 3, 1, -1, 0)]
+          (50, 8256, 64, 3, 1, -1, 0), (150, 2688, 1408, 4, 2, -1, None), (90, 1152, 1536, 2, 2, -1, None),
+          (70, 2304, 1280, 3, 1, 40, None), (300, 1344, 1088, 2, 1, -1, None), (450, 448, 1344, 64, 2, -1, None),
+          (450, 1344, 704, 64, 2, -1, 5), (700, 640, 1408, 64, 2, -1, 3), (300, 1408, 640, 64, 4, -1, None)]
 
 
 def run_products(shape, form, dtype, seed=0):
