@@ -451,12 +451,13 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // kBytes (4 or 16) per lane straight to LDS: lane l's go to dst + l * kBytes.
 // (A device function: the host compilation does not know the 16-byte form.)
+// `at` is the same for all lanes; offset + at counts in the bounds check.
 template <int kBytes>
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, unsigned char* dst, int offset) {
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, unsigned char* dst, int offset, int at) {
   if constexpr (kBytes == 16)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)dst, 16, offset, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)dst, 16, offset, at, 0, 0);
   else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)dst, 4, offset, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)dst, 4, offset, at, 0, 0);
 }
 
 template <int N> __device__ __forceinline__ void wait_vmcnt_lgkm0() {
@@ -584,28 +585,27 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
     const unsigned src = static_cast<unsigned>(gn[i]) / static_cast<unsigned>(gdiv);
     return srow + 8 * i < t.rows && src < static_cast<unsigned>(src_rows) ? static_cast<int>(src) : -1;
   };
-  const uint8_t *w_base = nullptr, *x_base = nullptr, *cw_base = nullptr, *cx_base = nullptr;
-  int w_rows = 0, x_rows = 0, cw_rows = 0, cx_rows = 0;
+  __amdgpu_buffer_rsrc_t w_res, x_res;  // the streams' operand rows of their tile (none: loads give zero)
+  const uint8_t *cw_base = nullptr, *cx_base = nullptr;
+  int cw_rows = 0, cx_rows = 0;
   int w_ks = 0, x_ks = 0, c_chunk = 0, c_start = 0;  // next stage or chunk (and its first stage) of each stream's tile
   int w_slot = 0, x_slot = 0, c_slot = 0;
   auto to_w = [&](const TileCoord& t) {
     w_ks = 0;
-    w_base = o.wq + (static_cast<int64_t>(t.e) * N + t.n0) * wstride;
-    w_rows = t.rows > 0 ? min(N - t.n0, kBN) : 0;
+    w_res = resource(o.wq + (static_cast<int64_t>(t.e) * N + t.n0) * wstride,
+                     t.rows > 0 ? min(N - t.n0, kBN) * wstride : 0);
   };
   auto to_x = [&](const TileCoord& t) {
     x_ks = 0;
     if constexpr (kGather) {
-      x_base = o.xq;
-      x_rows = t.rows > 0 ? src_rows : 0;
+      x_res = resource(o.xq, t.rows > 0 ? src_rows * xstride : 0);
 #pragma unroll
       for (int i = 0; i < kLdX; ++i) {
         const int s = source(t, i);
         vx[i] = s < 0 ? kOutside : s * xstride + (((lane & 7) ^ key_x(srow + 8 * i)) << 4);
       }
     } else {
-      x_base = o.xq + static_cast<int64_t>(t.m0) * xstride;
-      x_rows = t.rows;
+      x_res = resource(o.xq + static_cast<int64_t>(t.m0) * xstride, t.rows * xstride);
     }
   };
   auto to_scales = [&](const TileCoord& t) {
@@ -632,24 +632,20 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
       cx_rows = t.rows;
     }
   };
-  auto rows_from = [&](const uint8_t* base, int rows, int stride, int at) {
-    return resource(base + at, max(rows * stride - at, 0));
-  };
+  // Where a stage's loads go, where in K they start, and whether it is the tile's last.
   struct Refill {
-    __amdgpu_buffer_rsrc_t xr, wr;
-    unsigned char *xd, *wd;
+    int xd, wd;  // LDS offsets
+    int xk, wk;
     bool last;
   };
   auto refill = [&]() {
-    return Refill{rows_from(x_base, x_rows, xstride, x_ks * kXRow), rows_from(w_base, w_rows, wstride, w_ks * kWRow),
-                  smem + P::kXAt + x_slot * P::kXUnit + wave * P::kRowsX * kXRow,
-                  smem + w_slot * P::kWUnit + wave * P::kRowsW * kWRow,
-                  x_ks + 1 == kstages};
+    return Refill{P::kXAt + x_slot * P::kXUnit + wave * P::kRowsX * kXRow, w_slot * P::kWUnit + wave * P::kRowsW * kWRow,
+                  x_ks * kXRow, w_ks * kWRow, x_ks + 1 == kstages};
   };
   // Load i of a stage's kLd: the token unit first.
   auto issue = [&](const Refill& f, int i) {
-    if (i < kLdX) load_lds<16>(f.xr, f.xd + i * 1024, f.last && past[i] ? kOutside : vx[i]);
-    else load_lds<16>(f.wr, f.wd + (i - kLdX) * 1024, vw[i - kLdX]);
+    if (i < kLdX) load_lds<16>(x_res, smem + f.xd + i * 1024, f.last && past[i] ? kOutside : vx[i], f.xk);
+    else load_lds<16>(w_res, smem + f.wd + (i - kLdX) * 1024, vw[i - kLdX], f.wk);
   };
   auto advance_w = [&]() {
     w_slot = w_slot + 1 == S::kWS ? 0 : w_slot + 1;
@@ -663,16 +659,17 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
   // past the range, which ends with a whole dword (an odd row's last one holds
   // 2 bytes of the row after it, or past the array's end: not used).
   auto issue_scales = [&]() {
-    const __amdgpu_buffer_rsrc_t wr = resource(cw_base + c_start * St::kScales, max((cw_rows * sstride + 3) / 4 * 4 - c_start * St::kScales, 0));
-    const __amdgpu_buffer_rsrc_t xr = resource(cx_base + c_start * St::kScales, max((cx_rows * sstride + 3) / 4 * 4 - c_start * St::kScales, 0));
+    const __amdgpu_buffer_rsrc_t wr = resource(cw_base, (cw_rows * sstride + 3) / 4 * 4);
+    const __amdgpu_buffer_rsrc_t xr = resource(cx_base, (cx_rows * sstride + 3) / 4 * 4);
+    const int at = c_start * St::kScales;
     unsigned char* wd = smem + P::kScaleAt + c_slot * P::kChunk + wave * P::kRowsW * kRun;
     unsigned char* xd = smem + P::kScaleAt + c_slot * P::kChunk + P::kChunkW + wave * P::kRowsX * kRun;
 #pragma unroll
     for (int run = 0; run < S::kRuns; ++run) {
 #pragma unroll
-      for (int i = 0; i < kTW; ++i) load_lds<4>(wr, wd + run * kBN * kRun + i * 256, vt[i] + run * kRun);
+      for (int i = 0; i < kTW; ++i) load_lds<4>(wr, wd + run * kBN * kRun + i * 256, vt[i], at + run * kRun);
 #pragma unroll
-      for (int i = 0; i < kLdX; ++i) load_lds<4>(xr, xd + run * kBM * kRun + i * 256, vs[i] + run * kRun);
+      for (int i = 0; i < kLdX; ++i) load_lds<4>(xr, xd + run * kBM * kRun + i * 256, vs[i], at + run * kRun);
     }
     c_slot ^= 1;
     c_start += chunk_base + (c_chunk < chunk_more ? 1 : 0);
@@ -722,37 +719,62 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
     const int c = kFmt == kMxFp4 ? kk * 2 + half : kk * 4 + 2 * hi + half;
     return *reinterpret_cast<const u32x4_t*>(smem + r_x * P::kXUnit + j * S::kWM * 32 * kXRow + (x_at + ((c ^ kx) << 4)));
   };
-  // Scales of a row this stage: `at` is its place in the chunk's first run, `rows` those of a run, `odd` whether
-  // its scales start 2 bytes into their dword.
-  auto read_scale = [&](int at, int rows, uint32_t mask, int odd) {
-    const int first_byte = r_cs * St::kScales;
-    auto word = [&](int b) {
-      return reinterpret_cast<const uint32_t*>(smem + P::kScaleAt + r_c * P::kChunk + at + (b / kRun) * rows * kRun +
-                                               b % kRun);
-    };
-    uint32_t lo, hi = 0;
-    if constexpr (kOdd) {
-      const uint32_t w0 = *word(first_byte), w1 = *word(first_byte + 4);
-      lo = __builtin_amdgcn_alignbit(w1, w0, 16 * odd);
-      if constexpr (kFmt == kMxFp4) hi = __builtin_amdgcn_alignbit(*word(first_byte + 8), w1, 16 * odd);
-    } else if constexpr (kFmt == kMxFp4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(word(first_byte));
-      lo = v.x;
-      hi = v.y;
-    } else {
-      lo = *word(first_byte);
-    }
-    if constexpr (kFmt == kMxFp4) return __builtin_amdgcn_perm(hi, lo, half ? 0x07050301u : 0x06040200u) & mask;
-    else return (lo >> (8 * half)) & mask;
+  // The words of this stage's scales of a row, as they lie in LDS, and the
+  // scales of this lane's K blocks from them (odd: they start 2 bytes into
+  // their word).
+  struct Words {
+    uint32_t w[(kFmt == kMxFp4 ? 2 : 1) + (kOdd ? 1 : 0)];
   };
+  int s_w = 0, s_x = 0;  // LDS offsets of the stage's scales: of row 0's, weights and tokens
+  auto place_scales = [&]() {
+    const int b = r_cs * St::kScales, run = S::kRuns == 1 ? 0 : b / kRun;
+    s_w = P::kScaleAt + r_c * P::kChunk + b + run * (kBN - 1) * kRun;
+    s_x = P::kScaleAt + P::kChunkW + r_c * P::kChunk + b + run * (kBM - 1) * kRun;
+  };
+  auto fetch_scale = [&](int at, int rows) {
+    Words v;
+    constexpr int kN = sizeof(v.w) / 4;
+    if constexpr (!kOdd && kN == 2) {
+      const uint2 u = *reinterpret_cast<const uint2*>(smem + at);
+      v.w[0] = u.x;
+      v.w[1] = u.y;
+    } else {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        // with two runs a later word may be in the second
+        const int over = S::kRuns > 1 && r_cs * St::kScales % kRun + 4 * n >= kRun ? (rows - 1) * kRun : 0;
+        v.w[n] = *reinterpret_cast<const uint32_t*>(smem + at + 4 * n + over);
+      }
+    }
+    return v;
+  };
+  auto scale_of = [&](const Words& v, uint32_t mask, int odd) {
+    uint32_t lo = v.w[0], hi = 0;
+    if constexpr (kOdd) lo = __builtin_amdgcn_alignbit(v.w[1], lo, 16 * odd);
+    if constexpr (kFmt == kMxFp4) {
+      hi = v.w[1];
+      if constexpr (kOdd) hi = __builtin_amdgcn_alignbit(v.w[2], hi, 16 * odd);
+      return __builtin_amdgcn_perm(hi, lo, half ? 0x07050301u : 0x06040200u) & mask;
+    } else {
+      return (lo >> (8 * half)) & mask;
+    }
+  };
+  const int sw_at = (wn * kWF * 32 + wrow) * kRun;
+  const int sx_at = (wm * 32 + frow) * kRun;
   int x_odd[P::kNJ] = {};  // kOdd: whether the lane's token rows are odd rows of xs
-  auto read_scales = [&](auto nj_c, bool last) {
+  Words ww[kWF], xw[P::kNJ];
+  auto fetch_scales = [&](auto nj_c) {
+#pragma unroll
+    for (int i = 0; i < kWF; ++i) ww[i] = fetch_scale(s_w + sw_at + i * 32 * kRun, kBN);
+#pragma unroll
+    for (int j = 0; j < decltype(nj_c)::value; ++j) xw[j] = fetch_scale(s_x + sx_at + j * S::kWM * 32 * kRun, kBM);
+  };
+  auto finish_scales = [&](auto nj_c, bool last) {
     const uint32_t mask = last ? tail_mask : 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < kWF; ++i) sw[i] = read_scale((wn * kWF * 32 + i * 32 + wrow) * kRun, kBN, mask, wrow & 1);
+    for (int i = 0; i < kWF; ++i) sw[i] = scale_of(ww[i], mask, wrow & 1);
 #pragma unroll
-    for (int j = 0; j < decltype(nj_c)::value; ++j)
-      sx[j] = read_scale(P::kChunkW + ((j * S::kWM + wm) * 32 + frow) * kRun, kBM, mask, x_odd[j]);
+    for (int j = 0; j < decltype(nj_c)::value; ++j) sx[j] = scale_of(xw[j], mask, x_odd[j]);
   };
   auto barrier = [&]() {
     asm volatile("" ::: "memory");
@@ -793,15 +815,15 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
       xlo[j] = read_x(0, j, 0);
       if constexpr (kFmt == kMxFp8) xhi[j] = read_x(0, j, 1);
     }
-    read_scales(nj_c, false);
+    place_scales();
+    fetch_scales(nj_c);
+    finish_scales(nj_c, false);
 
     // One k-step: its kWF NJ MFMAs, each token fragment replaced by that of
     // `next` once used, and (last) the loads that refill the freed slots.
-    auto block = [&](auto kk_c, auto next_c, auto last_c, u32x4_t (&wa)[kWF], u32x4_t (&wb)[kWF]) {
+    auto block = [&](auto kk_c, auto next_c, auto last_c, const Refill& f, u32x4_t (&wa)[kWF], u32x4_t (&wb)[kWF]) {
       constexpr int kk = decltype(kk_c)::value, next = decltype(next_c)::value;
       constexpr int kSel = kFmt == kMxFp4 ? kk : 2 * kk;
-      Refill f;
-      if constexpr (decltype(last_c)::value) f = refill();
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
 #pragma unroll
@@ -829,24 +851,20 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
       using std::integral_constant;
       constexpr integral_constant<bool, false> no{};
       constexpr integral_constant<bool, true> yes{};
-      block(integral_constant<int, 0>{}, integral_constant<int, 1>{}, no, wf[0], wf[1]);
-      if constexpr (kSteps == 4) {
-        block(integral_constant<int, 1>{}, integral_constant<int, 2>{}, no, wf[1], wf[0]);
-        block(integral_constant<int, 2>{}, integral_constant<int, 3>{}, no, wf[0], wf[1]);
-      }
-      // The next stage must have landed.  lgkmcnt(0): this wave's reads of the
-      // stage are complete, so after the barrier its units are free.
-      if (S::kWS > S::kXS && kstages < S::kWS) wait_vmcnt_lgkm0<P::kInFlightShort>();
-      else wait_vmcnt_lgkm0<P::kInFlight>();
-      barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      // The first stage of a scale chunk: the other chunk slot is free.
-      if (r_cs == 0) {
-        if (c_chunk == nchunks) to_scales(nxt);
-        issue_scales();
-      }
+      // scalar work before the wait, in the MFMAs' shadow
       if (x_ks == kstages) to_x(nxt);
       if (w_ks == kstages) to_w(nxt);
+      Refill f = refill();
+      advance_x();
+      advance_w();
+      block(integral_constant<int, 0>{}, integral_constant<int, 1>{}, no, f, wf[0], wf[1]);
+      if constexpr (kSteps == 4) {
+        block(integral_constant<int, 1>{}, integral_constant<int, 2>{}, no, f, wf[1], wf[0]);
+        block(integral_constant<int, 2>{}, integral_constant<int, 3>{}, no, f, wf[0], wf[1]);
+      }
+      // (and before the barrier: the asm statements keep the compiler from
+      // putting it off until every wave waits for it)
+      const bool chunk_begins = r_cs == 0;
       r_w = r_w + 1 == S::kWS ? 0 : r_w + 1;
       r_x = r_x + 1 == S::kXS ? 0 : r_x + 1;
       if (++r_cs == chunk_base + (r_chunk < chunk_more ? 1 : 0)) {
@@ -854,10 +872,23 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
         r_c ^= 1;
         r_chunk = r_chunk + 1 == nchunks ? 0 : r_chunk + 1;
       }
-      block(integral_constant<int, kSteps - 1>{}, integral_constant<int, 0>{}, yes, wf[1], wf[0]);
-      advance_x();
-      advance_w();
-      read_scales(nj_c, ks + 2 == kstages);
+      place_scales();
+      asm volatile("" : "+s"(r_w), "+s"(r_x), "+s"(r_c), "+s"(r_cs), "+s"(s_w), "+s"(s_x));
+      asm volatile("" : "+s"(f.xd), "+s"(f.wd), "+s"(f.xk), "+s"(f.wk));
+      // The next stage must have landed.  lgkmcnt(0): this wave's reads of the
+      // stage are complete, so after the barrier its units are free.
+      if (S::kWS > S::kXS && kstages < S::kWS) wait_vmcnt_lgkm0<P::kInFlightShort>();
+      else wait_vmcnt_lgkm0<P::kInFlight>();
+      barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      // The first stage of a scale chunk: the other chunk slot is free.
+      if (chunk_begins) {
+        if (c_chunk == nchunks) to_scales(nxt);
+        issue_scales();
+      }
+      fetch_scales(nj_c);
+      block(integral_constant<int, kSteps - 1>{}, integral_constant<int, 0>{}, yes, f, wf[1], wf[0]);
+      finish_scales(nj_c, ks + 2 == kstages);
     }
 
     // acc[i][j][q]: tile row (j kWM + wm)*32 + frow, column (wn kWF + i)*32 + 16 half + q.
