@@ -838,7 +838,6 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
 #pragma unroll
           for (int l = j * kLd / NJ; l < (j + 1) * kLd / NJ; ++l) issue(f, l);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
       // Pin the accumulators here: the compiler would else sink the MFMAs
       // past the stage's branches to its end, with every fragment live.
