@@ -84,20 +84,28 @@ __device__ __forceinline__ float mx_decode_fp4(uint32_t c) {
   return (c & 8u) ? -v : v;
 }
 
-// 8 codes to fp32 values (before the scale).
-template <int kFmt> __device__ __forceinline__ void mx_load8(const uint8_t* codes, int64_t at, float* v) {
+// The 4 e4m3 codes of a dword to fp32.
+__device__ __forceinline__ void mx_decode4_fp8(uint32_t r, float* v) {
+  const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r), false);
+  const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r), true);
+  v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
+}
+
+// 8 or 4 codes, the first of element `at`, to fp32 values (before the scale).
+template <int kFmt, int kEl> __device__ __forceinline__ void mx_load(const uint8_t* codes, int64_t at, float* v) {
+  static_assert(kEl == 8 || kEl == 4, "");
   if constexpr (kFmt == kMxFp4) {
-    const uint32_t r = *reinterpret_cast<const uint32_t*>(codes + at / 2);
+    uint32_t r;
+    if constexpr (kEl == 8) r = *reinterpret_cast<const uint32_t*>(codes + at / 2);
+    else r = *reinterpret_cast<const uint16_t*>(codes + at / 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = mx_decode_fp4(r >> (4 * i));
-  } else {
+    for (int i = 0; i < kEl; ++i) v[i] = mx_decode_fp4(r >> (4 * i));
+  } else if constexpr (kEl == 8) {
     const uint2 r = *reinterpret_cast<const uint2*>(codes + at);
-    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.x), false);
-    const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.x), true);
-    const f32x2_t c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.y), false);
-    const f32x2_t d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(r.y), true);
-    v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
-    v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
+    mx_decode4_fp8(r.x, v);
+    mx_decode4_fp8(r.y, v + 4);
+  } else {
+    mx_decode4_fp8(*reinterpret_cast<const uint32_t*>(codes + at), v);
   }
 }
 
@@ -118,12 +126,13 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
     v[4 + i] = __uint_as_float(b[i]);
   }
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+__device__ __forceinline__ u32x4_t pack8_bf16(const float* v) {
   u32x4_t r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  st16(p, r);
+  return r;
 }
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) { st16(p, pack8_bf16(v)); }
 __device__ __forceinline__ void store8(float* p, const float* v) {
   u32x4_t a, b;
 #pragma unroll
@@ -134,6 +143,11 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   st16(p, a);
   st16(p + 4, b);
 }
+
+// For values that nothing reads soon.  fp32 goes through the caches: a lane's
+// two stores touch every other 16 bytes, and the caches join them.
+__device__ __forceinline__ void store8_nt(uint16_t* p, const float* v) { st16_nt(p, pack8_bf16(v)); }
+__device__ __forceinline__ void store8_nt(float* p, const float* v) { store8(p, v); }
 
 // The codes of 16 consecutive elements, the first of them element `at` (a
 // multiple of 16): one 8-byte (e2m1) or 16-byte (e4m3) store.
