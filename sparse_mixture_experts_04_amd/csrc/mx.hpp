@@ -149,18 +149,6 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
 __device__ __forceinline__ void store8_nt(uint16_t* p, const float* v) { st16_nt(p, pack8_bf16(v)); }
 __device__ __forceinline__ void store8_nt(float* p, const float* v) { store8(p, v); }
 
-// The codes of 16 consecutive elements, the first of them element `at` (a
-// multiple of 16): one 8-byte (e2m1) or 16-byte (e4m3) store.
-template <int kFmt>
-__device__ __forceinline__ void mx_store16(uint8_t* codes, int64_t at, const float* v, float inv, bool bad) {
-  if constexpr (kFmt == kMxFp4) {
-    *reinterpret_cast<uint2*>(codes + at / 2) = make_uint2(mx_encode8_fp4(v, inv, bad), mx_encode8_fp4(v + 8, inv, bad));
-  } else {
-    st16(codes + at, u32x4_t{mx_encode4_fp8(v, inv, bad), mx_encode4_fp8(v + 4, inv, bad),
-                             mx_encode4_fp8(v + 8, inv, bad), mx_encode4_fp8(v + 12, inv, bad)});
-  }
-}
-
 // Largest abs_bits over the 4 lanes that hold a block (8 elements each).
 __device__ __forceinline__ uint32_t mx_block_max(const float* v) {
   uint32_t m = abs_bits(v[0]);

@@ -393,9 +393,16 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
 // * Where K ends inside a stage, the token chunks past it are loaded as zero
 //   and the scales past it are masked, so what the weight unit holds there
 //   (e2m1 codes are all finite) adds nothing.
-// Measured on MI355X, Big: 1.72 PFLOP/s with e4m3 rows (8192 tokens, d = 2048,
-// F = 5632, 32 experts, k = 2: both products 0.44 ms) and 2.83 PFLOP/s with e2m1 rows (16384 tokens, d = 4096, F =
-// 14336, 64 experts, k = 2: 2.72 ms).
+// Measured on MI355X, Big, both products: e4m3 rows, d = 2048, F = 5632, 32
+// experts, k = 2: 0.46 ms at 8192 tokens (1.63 PFLOP/s; 2.5 tiles per CU in the
+// down projection, so the last round of tiles runs half full), 1.48 ms at 32768
+// (2.05); e2m1 rows, d = 4096, F = 14336, 64 experts, k = 2: 2.45 ms at 16384
+// tokens (3.15).  A stage's MFMAs take about 60 % of its cycles; the waits for
+// data 2 to 5 % (e2m1 up to 18), the barrier 16 % and the up-projection's
+// epilogue 18 %.  Tried and slower: a block's tiles as one contiguous run of
+// equal cost (8192 tokens: 0.50 ms; neighbouring tiles then no longer run at the
+// same time and share the L2), scales in LDS with a swizzle against bank
+// conflicts (2.74 ms), 128 x 192 tiles in two blocks per CU (1.54 ms at 32768).
 constexpr int kXRow = 128;  // bytes of a token row per stage
 constexpr int kRun = 32;    // bytes of a row's scales that one load covers
 template <int kFmt> struct Stage {
@@ -1006,10 +1013,16 @@ hipError_t launch_few(const MxOperands& o, const int32_t* gidx, int gdiv, int sr
 //   fp4  few             38   117   157   209   272   447
 //        Mid             66   177   184   185   207   260
 //        Big             59   178   183   184   189   213
-// and for one expert (d = F = 2048, fp8) of 100, 200, 400, 3000 rows: few 19, 25, 38, 174, Mid 25, 26, 27, 59, Big 42,
-// 65, 65, 69; fp4, 5000 rows: few 239, Mid 80, Big 55.
+// and for one expert (d = F = 2048):
+//   rows                100   200   400  3000  4000  6000  8000
+//   fp8  few             19    25    38   174
+//        Mid             25    26    27    58    61    83   106
+//        Big             42    65    65    71    72    74    80
+//   fp4  Mid                               46    57    78    97
+//        Big                               49    52    54    59
 //   few: weights dominate, or all its blocks run at once;
-//   Mid: too few tiles for Big to fill the CUs (half of them, for e2m1 rows);
+//   Mid: its tiles (an expert's last one half full) are at most two rounds of
+//   the two blocks per CU, three for e2m1 rows, whose tiles are half as wide;
 //   few also takes what the tiled kernels do not: K shorter than their rings, rows past 32-bit offsets.
 template <int kFmt, bool kGather, typename Out>
 hipError_t launch_product(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
@@ -1021,10 +1034,10 @@ hipError_t launch_product(const MxOperands& o, const int32_t* gidx, int gdiv, in
   const bool few = rows <= (kFmt == kMxFp4 ? 12 : 6) * active ||
                    (rows / few_chunk(o) + active) * (o.N / kFewRows) <= 3 * cus;
   if (!few) {
-    const int64_t big_m = (rows + BigShape<kFmt>::kBM - 1) / BigShape<kFmt>::kBM;
-    const int64_t big = (big_m > active ? big_m : active) * ((o.N + BigShape<kFmt>::kBN - 1) / BigShape<kFmt>::kBN);
-    if (big <= (kFmt == kMxFp4 ? cus / 2 : cus) && tiled_runs<MidShape<kFmt>>(o, kGather, src_rows))
-      return launch_tiled<MidShape<kFmt>, kGather>(o, gidx, gdiv, src_rows, out, stream);
+    using Mid = MidShape<kFmt>;
+    const int64_t mid = (rows / Mid::kBM + (active + 1) / 2) * ((o.N + Mid::kBN - 1) / Mid::kBN);
+    if (mid <= (kFmt == kMxFp4 ? 6 : 4) * cus && tiled_runs<Mid>(o, kGather, src_rows))
+      return launch_tiled<Mid, kGather>(o, gidx, gdiv, src_rows, out, stream);
     if (tiled_runs<BigShape<kFmt>>(o, kGather, src_rows))
       return launch_tiled<BigShape<kFmt>, kGather>(o, gidx, gdiv, src_rows, out, stream);
   }
