@@ -40,7 +40,9 @@
  *     NaN); the elements are codes of 4 bits (e2m1, two to a byte, the even
  *     element in the low nibble) or 8 bits (e4m3).  Codes [rows, n/2] or
  *     [rows, n] bytes and scales [rows, n/32] bytes, both row-major.  Pointers
- *     of the MX entry points must be 16-byte aligned.
+ *     of the MX entry points must be 16-byte aligned.  The aligned 4-byte word
+ *     that holds an array's last scales may be read whole; what lies past the
+ *     scales in it is not used.
  *
  * Limits: 1 <= E <= 64; 1 <= k <= E; d and F positive multiples of 64;
  * T >= 0 (T = 0 is a no-op); T*k*max(d, F) < 2^62 elements.

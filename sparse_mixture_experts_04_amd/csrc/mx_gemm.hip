@@ -165,6 +165,9 @@ template <typename T> struct DownOut {
 // window, 16 KB, before the first MFMA: with about 12 waves on a CU 192 KB of
 // weights are on their way.  The chunks of one expert's weight rows are
 // neighbours on one XCD, so its L2 serves the weights to all but the first.
+// Measured on MI355X, both products (d = 3584, F = 2560, 64 experts, k = 2): one
+// token, e4m3, 13.3 us (6.9 + 5.8, of which a launch alone takes about 3 each);
+// 8 tokens, e2m1, 34.6 us: 140 MB at 4.05 TB/s.
 //
 // One 16x16x128 scaled MFMA takes 8 weight rows x 2 K-slices (operand A) and 8
 // token rows x the same 2 slices (operand B); of its 16x16 results those of
@@ -940,8 +943,8 @@ __global__ __launch_bounds__((Plan<S, kOdd>::kWaves * kWave)) void mx_product_ti
 }
 
 // The tiled kernels take K at least the token ring long and 32-bit buffer
-// offsets: a tile's rows of K
-// and of the result, and where rows are gathered all of them, below 2^31 bytes.
+// offsets: a tile's rows of K and of the result, and where rows are gathered
+// all of them, below 2^31 bytes.
 template <typename S> bool tiled_runs(const MxOperands& o, bool gather, int src_rows) {
   constexpr int64_t kLimit = int64_t{1} << 31;
   return o.K > (S::kXS - 1) * Stage<S::kFmt>::kK && int64_t{256} * o.K < kLimit &&

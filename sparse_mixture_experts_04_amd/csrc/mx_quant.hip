@@ -8,8 +8,9 @@
 // one rounding, so codes and scales are the definition's, bit for bit.
 // All three kernels are bound by memory: each element is touched once, and the
 // four lanes of a block exchange their maxima in registers.  At 180224 x 2048
-// bf16 e2m1 quantises in 155 us (6.0 TB/s) and comes back in 138 us (6.8); e4m3
-// takes 186 and 171 us (6.0, 6.5).  8 x 3584, 3 to 4 us each, is one launch.
+// bf16 <-> e2m1, 0.93 GB each way, quantising takes 154 us (6.1 TB/s) and the
+// way back 224 us (4.2; 138 where the codes are still in the last-level
+// cache); a copy of 4 GiB runs at 4.7.  8 x 3584 takes one launch, 2.5 us.
 #include "kernels.hpp"
 #include "mx.hpp"
 
@@ -38,8 +39,8 @@ __global__ __launch_bounds__(kQThreads) void mx_quantize_kernel(const T* __restr
 // One 16-byte store per thread and so 8 bf16 or 4 f32 values each: a wave's
 // stores lie side by side, which non-temporal stores need (f32 with two stores
 // per lane, 32 bytes apart: 208 us at 65536 x 2048, against 93).  The values are
-// two to eight times the bytes read; through the caches e2m1 to bf16 took 231 us
-// at 180224 x 2048, past them 138.
+// two to eight times the bytes read; through the caches e2m1 to bf16 took 230 us
+// at 180224 x 2048 against 224, and the quantisation after it 176 against 154.
 template <typename T, int kFmt>
 __global__ __launch_bounds__(kQThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales,
