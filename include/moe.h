@@ -311,7 +311,8 @@ moe_status moe_forward_noalloc(const moe_config* cfg, const void* X, const void*
  * rounded to nearest even and saturated to +-6 or +-448.  A block that holds a
  * NaN or an infinity gets scale 255 and zero codes (all NaN when read back).
  *   X [rows, cols] of dtype in; codes [rows, cols/2] or [rows, cols] bytes and
- *   scales [rows, cols/32] out.  rows >= 0, cols a multiple of 32. */
+ *   scales [rows, cols/32] out.  rows >= 0, cols a multiple of 32.  The three
+ *   arrays may not overlap (refused), here and in moe_mx_dequantize. */
 moe_status moe_mx_quantize(int32_t dtype, int32_t format, int64_t rows, int64_t cols, const void* X,
                            void* codes, uint8_t* scales, void* stream);
 
@@ -367,6 +368,7 @@ moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t format, const void* 
  * for the experts), moe_route on y, moe_dispatch, moe_expert_ffn_mx,
  * moe_combine.  residual and sum may be NULL; out [T, d] is the experts'
  * combined output (not added to sum: the next norm's addition does that).
+ * sum may be X or residual, and out may be either, but not sum (refused).
  * The other buffers as in moe_forward; the intermediates live in ws
  * (moe_workspace_size(cfg, MOE_OP_FORWARD_MX)). */
 moe_status moe_forward_mx(const moe_config* cfg, int32_t format, const void* X, const void* residual,

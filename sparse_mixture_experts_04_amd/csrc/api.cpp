@@ -111,6 +111,19 @@ moe_status check_mx(int32_t dtype, int32_t format, int64_t rows, int64_t cols) {
   return MOE_OK;
 }
 
+// Whether two ranges share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < na : x - y < nb;
+}
+
+// Array, codes and scales of n elements: none may reach into another, since
+// the quantisation and its inverse run in no order.
+bool mx_overlap(int32_t dtype, int32_t format, size_t n, const void* x, const void* codes, const void* scales) {
+  const size_t nx = n * (dtype == MOE_BF16 ? 2 : 4), nc = format == MOE_MXFP4 ? n / 2 : n;
+  return overlap(x, nx, codes, nc) || overlap(x, nx, scales, n / 32) || overlap(codes, nc, scales, n / 32);
+}
+
 moe::MxOperands mx_operands(const moe_config* c, const void* xq, const uint8_t* xs, const void* wq, const uint8_t* ws,
                             const int32_t* offsets, int N, int K) {
   return moe::MxOperands{static_cast<const uint8_t*>(xq), xs, static_cast<const uint8_t*>(wq), ws, offsets,
@@ -442,6 +455,7 @@ moe_status moe_mx_quantize(int32_t dtype, int32_t format, int64_t rows, int64_t 
   if (moe_status s = check_mx(dtype, format, rows, cols); s != MOE_OK) return s;
   if (rows == 0 || cols == 0) return MOE_OK;
   if (!X || !codes || !scales || !aligned16(X, codes, scales)) return MOE_ERR_INVALID_ARG;
+  if (mx_overlap(dtype, format, static_cast<size_t>(rows * cols), X, codes, scales)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_mx_quantize(dtype, format, X, codes, scales, rows * cols, as_stream(stream)));
 }
 
@@ -450,6 +464,7 @@ moe_status moe_mx_dequantize(int32_t dtype, int32_t format, int64_t rows, int64_
   if (moe_status s = check_mx(dtype, format, rows, cols); s != MOE_OK) return s;
   if (rows == 0 || cols == 0) return MOE_OK;
   if (!X || !codes || !scales || !aligned16(X, codes, scales)) return MOE_ERR_INVALID_ARG;
+  if (mx_overlap(dtype, format, static_cast<size_t>(rows * cols), X, codes, scales)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_mx_dequantize(dtype, format, codes, scales, X, rows * cols, as_stream(stream)));
 }
 
@@ -525,6 +540,7 @@ moe_status moe_forward_mx(const moe_config* cfg, int32_t format, const void* X, 
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < forward_mx_bytes(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (ws == nullptr || !aligned16(X, residual, gamma, W1q, W1s, W2q, W2s, sum, out, ws)) return MOE_ERR_INVALID_ARG;
+  if (cfg->num_tokens > 0 && sum == out) return MOE_ERR_INVALID_ARG;
   const size_t t = static_cast<size_t>(cfg->num_tokens);
   uint8_t* p = static_cast<uint8_t*>(ws);
   auto take = [&p](size_t bytes) {

@@ -9,6 +9,7 @@
 // (v_mfma_scale_f32_*_f8f6f4) and accumulate in fp32: nothing is widened in
 // memory.  The up-projection's GELU and the quantisation of its result to the
 // next product's operand run on the accumulators.
+#include <atomic>
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -955,10 +956,18 @@ template <typename S, bool kGather, bool kOdd, typename Out>
 hipError_t launch_tiled(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
                         hipStream_t stream) {
   using P = Plan<S, kOdd>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_product_tiled<S, kGather, kOdd, Out>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::kLds));
-  if (attr != hipSuccess) return attr;
+  // once per device (of the first 64; past them at every launch)
+  static std::atomic<uint64_t> allowed{0};
+  int device = 0;
+  if (hipError_t e = hipGetDevice(&device); e != hipSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_product_tiled<S, kGather, kOdd, Out>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::kLds));
+        e != hipSuccess)
+      return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   // at most this many tiles
   const int64_t tiles = (static_cast<int64_t>((o.max_rows + S::kBM - 1) / S::kBM) + o.E) * ((o.N + S::kBN - 1) / S::kBN);
   if (tiles > 0x7fffffff) return hipErrorInvalidValue;

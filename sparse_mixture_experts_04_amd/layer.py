@@ -127,8 +127,14 @@ def mx_quantize(x: torch.Tensor, fmt: int = _lib.MOE_MXFP4, stream=None):
 def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt: int = _lib.MOE_MXFP4, dtype=torch.bfloat16,
                   stream=None) -> torch.Tensor:
     """The values of microscaled codes and scales, as mx_quantize gives them."""
-    x = torch.empty((*scales.shape[:-1], scales.shape[-1] * 32), dtype=dtype, device=codes.device)
-    n = x.shape[-1]
+    if fmt not in (_lib.MOE_MXFP4, _lib.MOE_MXFP8):
+        raise ValueError(f"fmt must be MOE_MXFP4 or MOE_MXFP8, not {fmt!r}")
+    n = scales.shape[-1] * 32
+    expected = (*scales.shape[:-1], n // 2 if fmt == _lib.MOE_MXFP4 else n)
+    if tuple(codes.shape) != expected:
+        raise ValueError(f"codes of shape {tuple(codes.shape)} do not go with scales of shape {tuple(scales.shape)}: "
+                         f"expected {expected}")
+    x = torch.empty((*scales.shape[:-1], n), dtype=dtype, device=codes.device)
     _lib.moe_mx_dequantize(_mx_kind(x), fmt, x.numel() // n if n else 0, n, codes, scales, x, stream=stream)
     return x
 

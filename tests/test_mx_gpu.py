@@ -354,3 +354,122 @@ def test_values_through_torch_types():
     w = moe.mx_dequantize(c.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu), moe.MOE_MXFP8, torch.float32)
     ref = c.view(torch.float8_e4m3fn).float().view(16, 8, 32) * s.view(torch.float8_e8m0fnu).float().unsqueeze(-1)
     assert torch.equal(v, w) and torch.equal(v, ref.view(16, 256))
+
+
+# Sizes whose byte or element offsets pass 32 bits.  Only sampled rows and columns are compared, the last ones among
+# them: an offset that wrapped would read or write elsewhere.
+
+def random_codes(rows, cols, fmt):
+    """Random finite codes and moderate scales, made on the GPU."""
+    c, s = code_buffers(rows, cols, fmt)
+    c.random_(0, 256) if fmt == moe.MOE_MXFP4 else c.random_(0, 120)
+    return c, s.random_(118, 125)
+
+
+@pytest.mark.parametrize("T", [4, 700])
+@pytest.mark.parametrize("form", ["fp4", "fp8"])
+def test_weights_past_32_bit_offsets(T, form):
+    d, F, E, k, fmt = 8192, 16384, 64, 2, FMT[form]
+    cfg = moe.config(T, d, F, E, k, -1, "bf16")
+    xq, xs = random_codes(T, d, fmt)
+    w1, w2 = random_codes(E * F, d, moe.MOE_MXFP4), random_codes(E * d, F, moe.MOE_MXFP4)
+    for w, K in ((w1, d), (w2, F)):  # results of order 1
+        w[1].sub_(int(0.5 * np.log2(K)))
+    assert w1[0].numel() > 2 ** 31 and w2[0].numel() > 2 ** 31
+    perm = np.concatenate([np.arange(T) * 2, np.arange(T) * 2 + 1]).astype(np.int32)  # every token: experts 1 and 63
+    offsets = np.array([0, 0] + [T] * 62 + [2 * T], dtype=np.int32)
+    p, o = to_dev(perm, offsets)
+    hq, hs = code_buffers(T * k, F, fmt)
+    moe.moe_expert_up_mx(cfg, fmt, xq, xs, p, o, *w1, hq, hs)
+    y = torch.full((T * k, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_down_mx(cfg, fmt, hq, hs, o, *w2, y)
+    torch.cuda.synchronize()
+    rows = {1: [0, T - 1], 63: [T, 2 * T - 1]}
+    for e in (1, 63):
+        r = rows[e]
+        for n0 in (0, F - 64):
+            at = slice(e * F + n0, e * F + n0 + 64)
+            xv = read(xq, xs, fmt)[2][perm[r] // 2]
+            u, total, peak = ox.product(xv, read(w1[0][at], w1[1][at], 0)[2])
+            bound = 1.13 * product_error(total, peak, d, fmt) + 2.0 ** -20 * np.abs(u)
+            c, s, _ = read(hq[r], hs[r], fmt)
+            check_codes(c[:, n0:n0 + 64], s[:, n0 // 32:n0 // 32 + 2], gelu_tanh(u), bound, fmt, f"expert {e} from {n0}")
+        for n0 in (0, d - 64):
+            at = slice(e * d + n0, e * d + n0 + 64)
+            yr, total, peak = ox.product(read(hq[r], hs[r], fmt)[2], read(w2[0][at], w2[1][at], 0)[2])
+            bound = product_error(total, peak, F, fmt) + HALF["bf16"] * 1.01 * np.abs(yr)
+            assert (np.abs(f64(y[r, n0:n0 + 64]) - yr) <= bound).all(), (e, n0)
+
+
+def test_gathered_rows_past_32_bit_offsets():
+    T, d, F, fmt = 262147, 8192, 64, moe.MOE_MXFP8
+    cfg = moe.config(T, d, F, 2, 1, -1, "bf16")
+    xq, xs = random_codes(T, d, fmt)
+    assert xq.numel() > 2 ** 31
+    w1 = random_codes(2 * F, d, moe.MOE_MXFP4)
+    w1[1].sub_(6)
+    half = T // 2
+    perm = np.concatenate([np.arange(half, T), np.arange(half)]).astype(np.int32)  # the late tokens: expert 0
+    p, o = to_dev(perm, np.array([0, T - half, T], dtype=np.int32))
+    hq, hs = code_buffers(T, F, fmt)
+    moe.moe_expert_up_mx(cfg, fmt, xq, xs, p, o, *w1, hq, hs)
+    torch.cuda.synchronize()
+    for e, r in ((0, [0, T - half - 2, T - half - 1]), (1, [T - half, T - 1])):
+        tokens = torch.from_numpy(perm[r]).long().cuda()
+        u, total, peak = ox.product(read(xq[tokens], xs[tokens], fmt)[2],
+                                    read(w1[0][e * F:(e + 1) * F], w1[1][e * F:(e + 1) * F], 0)[2])
+        bound = 1.13 * product_error(total, peak, d, fmt) + 2.0 ** -20 * np.abs(u)
+        c, s, _ = read(hq[r], hs[r], fmt)
+        check_codes(c, s, gelu_tanh(u), bound, fmt, f"expert {e}")
+
+
+def test_rows_past_32_bit_offsets():
+    """The last rows of arrays of more than 2^31 elements have the bits of the same rows alone."""
+    rows, d = 131075, 16384
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[-5:] = torch.randn(5, d, device="cuda").bfloat16()
+    last = x[-5:].clone()
+    for fmt in (moe.MOE_MXFP4, moe.MOE_MXFP8):
+        c, s = moe.mx_quantize(x, fmt)
+        c2, s2 = moe.mx_quantize(last, fmt)
+        assert torch.equal(c[-5:], c2) and torch.equal(s[-5:], s2)
+        assert torch.equal(moe.mx_dequantize(c, s, fmt)[-5:], moe.mx_dequantize(c2, s2, fmt))
+    g = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    results = []
+    for t in (x, last):
+        total, y = torch.empty_like(t), torch.empty_like(t)
+        c, s = code_buffers(t.shape[0], d, moe.MOE_MXFP8)
+        moe.moe_add_rmsnorm(moe.config(t.shape[0], d, 64, 1, 1, -1, "bf16"), t, t, g, EPS, total, y, moe.MOE_MXFP8, c, s)
+        results.append([v[-5:].clone() for v in (total, y, c, s)])
+        del total, y, c, s
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("T,form", [(6, "fp4"), (300, "fp8")])
+@pytest.mark.parametrize("sum_is,out_is", [("x", None), ("r", None), (None, "x"), (None, "r"), ("x", "r"), ("r", "x")])
+def test_layer_in_place(T, form, sum_is, out_is):
+    """sum and out may be the buffers of X and the residual: the same bits."""
+    layer, x, r = make_layer(T, 256, 192, 8, 2, form)
+    out, total = layer.forward(x, r).clone(), layer.sum.clone()
+    b, own = layer.buf, {"x": x.clone(), "r": r.clone()}
+    s, o = own.get(sum_is, layer.sum), own.get(out_is, b.out)
+    moe.moe_forward_mx(layer.cfg, layer.fmt, own["x"], own["r"], layer.gamma, layer.eps, layer.Wg, layer.gate_bias,
+                       *layer.W1, *layer.W2, s, o, b.topk_ids, b.topk_w, b.expert_counts, b.expert_offsets, b.perm,
+                       b.inv_perm, b.ws)
+    assert torch.equal(s, total) and torch.equal(o, out)
+
+
+def test_two_layers_on_two_streams():
+    """Calls with buffers of their own may run at the same time."""
+    (a, xa, ra), (c, xc, rc) = (make_layer(T, 512, 320, 8, 2, f) for T, f in ((300, "fp8"), (9, "fp4")))
+    ref = a.forward(xa, ra).clone(), c.forward(xc, rc).clone()
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        a.buf.out.zero_(), c.buf.out.zero_()
+        torch.cuda.synchronize()
+        for s, layer, x, r in ((streams[0], a, xa, ra), (streams[1], c, xc, rc)):
+            for _ in range(4):
+                layer.forward(x, r, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(a.buf.out, ref[0]) and torch.equal(c.buf.out, ref[1])

@@ -124,3 +124,35 @@ def test_tensors_are_checked():
         moe.mx_quantize(torch.zeros(4, 64, dtype=torch.float16))
     with pytest.raises(ValueError):
         moe.mx_quantize(x, fmt=4)
+
+
+@pytest.mark.parametrize("fn,order", [(moe.moe_mx_quantize, (0, 1, 2)), (moe.moe_mx_dequantize, (1, 2, 0))])
+@pytest.mark.parametrize("dtype,es", [(moe.MOE_BF16, 2), (moe.MOE_F32, 4)])
+@pytest.mark.parametrize("fmt", [moe.MOE_MXFP4, moe.MOE_MXFP8])
+def test_overlapping_arrays_are_refused(fn, order, dtype, es, fmt):
+    # 4 x 64 elements; each pair of (array, codes, scales) in turn shares its last or first 16 bytes
+    sizes = (256 * es, 256 // (2 if fmt == moe.MOE_MXFP4 else 1), 256 // 32)
+    apart = (1 << 20, 2 << 20, 3 << 20)
+    for a in range(3):
+        for b in range(3):
+            if a != b:
+                at = list(apart)
+                at[b] = apart[a] + (sizes[a] - 1) // 16 * 16
+                _refused(INVALID, fn, dtype, fmt, 4, 64, *[at[i] for i in order])
+
+
+def test_forward_refuses_one_buffer_for_sum_and_out():
+    cfg = moe.config(4, 128, 64, 2, 1, -1, "bf16")
+    need = moe.moe_workspace_size(cfg, moe.MOE_OP_FORWARD_MX)
+    at = [(i + 1) << 20 for i in range(17)]
+    _refused(INVALID, moe.moe_forward_mx, cfg, moe.MOE_MXFP8, *at[:3], 1e-5, *at[3:9], at[9], at[9], *at[10:], need)
+
+
+def test_codes_of_another_format_are_refused():
+    codes, scales = torch.zeros(3, 64, dtype=torch.uint8), torch.zeros(3, 2, dtype=torch.uint8)
+    for c, s, fmt in ((codes, scales, moe.MOE_MXFP4), (codes[:, :32], scales, moe.MOE_MXFP8),
+                      (codes[:2], scales, moe.MOE_MXFP8)):
+        with pytest.raises(ValueError, match="do not go with"):
+            moe.mx_dequantize(c, s, fmt)
+    with pytest.raises(ValueError, match="fmt must be"):
+        moe.mx_dequantize(codes, scales, 2)
