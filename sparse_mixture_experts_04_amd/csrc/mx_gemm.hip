@@ -372,9 +372,10 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_product_few(MxOperands o
 // two shapes:
 //   Big: 256 token rows x 256 weight rows, 8 waves of 128 x 64: the least
 //     traffic per product.
-//   Mid: 64 token rows x 128 weight rows, 4 waves of 64 x 32, with deep rings,
+//   Mid: 64 token rows x 128 weight rows (e2m1 rows: 64), 4 waves of 64 x 32,
 //     for experts of some dozen rows: bound by the weight stream and its
-//     latency, so more tiles and more stages in flight.
+//     latency, so more tiles and several blocks on a CU, with rings of 4 stages
+//     (two blocks) or of 2 (three).
 //
 // * A stage is 128 bytes of every token row (256 of K in e2m1, 128 in e4m3)
 //   and the same K of the weight rows.  LDS holds a ring of token units, a ring
@@ -421,9 +422,9 @@ template <int kFmt_> struct BigShape {
   static constexpr int kFmt = kFmt_, kBM = 256, kBN = 256, kWM = 2, kWN = 4, kXS = 2, kWS = kFmt_ == kMxFp4 ? 2 : 4,
                        kRuns = 1;
 };
-template <int kFmt_> struct MidShape {
+template <int kFmt_, int kRing> struct MidShape {
   static constexpr int kFmt = kFmt_, kBM = 64, kBN = kFmt_ == kMxFp4 ? 64 : 128, kWM = kFmt_ == kMxFp4 ? 2 : 1,
-                       kWN = 4 / kWM, kXS = 4, kWS = kXS, kRuns = kFmt_ == kMxFp4 ? 2 : 1;
+                       kWN = 4 / kWM, kXS = kRing, kWS = kRing, kRuns = kFmt_ == kMxFp4 ? 2 : 1;
 };
 // kOdd: K is an odd multiple of 64, so every second row of scales starts in the
 // middle of a dword.
@@ -1019,7 +1020,7 @@ hipError_t launch_few(const MxOperands& o, const int32_t* gidx, int gdiv, int sr
 // 2048, F = 1408, 32 experts, k = 4; fp4: d = 3584, F = 2560, 64 experts, k = 2):
 //   rows per expert       4     8    12    25    42    62    88
 //   fp8  few             32    38    46    62    82   107   134
-//        Mid             31    35    36    39    48    52    60
+//        Mid             31    35    36    38    42    49    53
 //        Big             43    45    46    46    51    57    65
 //   rows per expert       1     3     9    19    31    62
 //   fp4  few             38   117   157   209   272   447
@@ -1028,13 +1029,17 @@ hipError_t launch_few(const MxOperands& o, const int32_t* gidx, int gdiv, int sr
 // and for one expert (d = F = 2048):
 //   rows                100   200   400  3000  4000  6000  8000
 //   fp8  few             19    25    38   174
-//        Mid             25    26    27    58    61    83   106
+//        Mid             25    26    27    47    60    83   106
 //        Big             42    65    65    71    72    74    80
-//   fp4  Mid                               46    57    78    97
+//   fp4  Mid                               43    57    78    97
 //        Big                               49    52    54    59
 //   few: weights dominate, or all its blocks run at once;
 //   Mid: its tiles (an expert's last one half full) are at most two rounds of
-//   the two blocks per CU, three for e2m1 rows, whose tiles are half as wide;
+//   two blocks per CU, three for e2m1 rows, whose tiles are half as wide; with
+//   the short rings, three blocks per CU, where that saves a round (one expert,
+//   d = F = 2048: fp8, 3000 rows 57 -> 47 us, fp4 46 -> 43; 42 rows per expert as
+//   above 45.6 -> 42.5), not where it does not (2000 tokens, 8 experts, F = 5632,
+//   fp8: 68 with the deep rings, 80 with the short);
 //   few also takes what the tiled kernels do not: K shorter than their rings, rows past 32-bit offsets.
 template <int kFmt, bool kGather, typename Out>
 hipError_t launch_product(const MxOperands& o, const int32_t* gidx, int gdiv, int src_rows, const Out& out,
@@ -1046,10 +1051,18 @@ hipError_t launch_product(const MxOperands& o, const int32_t* gidx, int gdiv, in
   const bool few = rows <= (kFmt == kMxFp4 ? 12 : 6) * active ||
                    (rows / few_chunk(o) + active) * (o.N / kFewRows) <= 3 * cus;
   if (!few) {
-    using Mid = MidShape<kFmt>;
-    const int64_t mid = (rows / Mid::kBM + (active + 1) / 2) * ((o.N + Mid::kBN - 1) / Mid::kBN);
-    if (mid <= (kFmt == kMxFp4 ? 6 : 4) * cus && tiled_runs<Mid>(o, kGather, src_rows))
-      return launch_tiled<Mid, kGather>(o, gidx, gdiv, src_rows, out, stream);
+    using Deep = MidShape<kFmt, 4>;
+    using Short = MidShape<kFmt, 2>;
+    constexpr int kDeepPerCu = Plan<Deep, false>::kPerCu, kShortPerCu = Plan<Short, false>::kPerCu;
+    static_assert(kDeepPerCu == 2 && kShortPerCu == 3, "the rule below was measured with these");
+    const int64_t mid = (rows / Deep::kBM + (active + 1) / 2) * ((o.N + Deep::kBN - 1) / Deep::kBN);
+    if (mid <= (kFmt == kMxFp4 ? 6 : 4) * cus) {
+      auto rounds = [&](int per_cu) { return (mid + per_cu * cus - 1) / (per_cu * cus); };
+      if (rounds(kShortPerCu) < rounds(kDeepPerCu) && tiled_runs<Short>(o, kGather, src_rows))
+        return launch_tiled<Short, kGather>(o, gidx, gdiv, src_rows, out, stream);
+      if (tiled_runs<Deep>(o, kGather, src_rows))
+        return launch_tiled<Deep, kGather>(o, gidx, gdiv, src_rows, out, stream);
+    }
     if (tiled_runs<BigShape<kFmt>>(o, kGather, src_rows))
       return launch_tiled<BigShape<kFmt>, kGather>(o, gidx, gdiv, src_rows, out, stream);
   }

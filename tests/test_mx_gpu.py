@@ -473,3 +473,22 @@ def test_two_layers_on_two_streams():
                 layer.forward(x, r, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(a.buf.out, ref[0]) and torch.equal(c.buf.out, ref[1])
+
+
+# Batches whose tiles fill more than two and at most three blocks per CU (short rings): K an odd multiple of 64 in
+# either product, K of two stages, several chunks of scales, fp32 results
+SHORT = [(700, 1408, 1344, 64, 2, -1, None), (700, 192, 1408, 64, 2, -1, None), (700, 576, 1408, 64, 2, 30, None)]
+
+
+@pytest.mark.parametrize("shape", SHORT, ids=lambda s: "x".join(map(str, s[:5])))
+@pytest.mark.parametrize("form", ["fp4", "fp8"])
+def test_products_short_rings(shape, form):
+    run_products(shape, form, "bf16", seed=2)
+
+
+def test_products_short_rings_fp32_output():
+    run_products((300, 1408, 640, 64, 4, -1, None), "fp8", "f32", seed=3)
+
+
+def test_products_short_rings_long_k():
+    run_products((260, 2240, 5504, 4, 1, -1, None), "fp4", "bf16", seed=4)
