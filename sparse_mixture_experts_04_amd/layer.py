@@ -149,6 +149,12 @@ class MxMoELayer:
     def __init__(self, cfg: _lib.MoeConfig, gamma: torch.Tensor, Wg: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
                  gate_bias: Optional[torch.Tensor] = None, fmt: int = _lib.MOE_MXFP8, eps: float = 1e-5,
                  device="cuda"):
+        d, F, E = cfg.hidden_size, cfg.intermediate_size, cfg.num_experts
+        for name, t, shape in (("gamma", gamma, (d,)), ("W1", W1, (E, F, d)), ("W2", W2, (E, d, F))):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if fmt not in (_lib.MOE_MXFP4, _lib.MOE_MXFP8):
+            raise ValueError(f"fmt must be MOE_MXFP4 or MOE_MXFP8, not {fmt!r}")
         self.cfg, self.fmt, self.eps = cfg, fmt, eps
         self.gamma, self.Wg, self.gate_bias = gamma, Wg, gate_bias
         self.W1, self.W2 = mx_quantize(W1), mx_quantize(W2)  # (codes, scales)

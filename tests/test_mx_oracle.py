@@ -156,3 +156,14 @@ def test_codes_of_another_format_are_refused():
             moe.mx_dequantize(c, s, fmt)
     with pytest.raises(ValueError, match="fmt must be"):
         moe.mx_dequantize(codes, scales, 2)
+
+
+def test_layer_refuses_other_shapes():
+    cfg = moe.config(4, 128, 64, 2, 1, -1, "bf16")
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    ok = dict(gamma=z(128), Wg=z(128, 2), W1=z(2, 64, 128), W2=z(2, 128, 64))
+    for name, t in (("gamma", z(64)), ("W1", z(2, 128, 64)), ("W2", z(2, 64, 128)), ("W1", z(3, 64, 128))):
+        with pytest.raises(ValueError, match=f"{name} must have shape"):
+            moe.MxMoELayer(cfg, **{**ok, name: t})
+    with pytest.raises(ValueError, match="fmt must be"):
+        moe.MxMoELayer(cfg, **ok, fmt=3)
